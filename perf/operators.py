@@ -1,0 +1,436 @@
+"""What the attention operators are measured on: rotary positions, the 4-bit
+key/value cache's append, and attention over it for single tokens and prompts.
+
+`run` is one pass of one operator: the plain form in elementary torch
+operations, or (where `own` is set) the library's call. Shapes are those of
+the decoder whose projections this repository multiplies (20 query heads, 5
+key/value heads of 128) and generic ones around them.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda"
+THETA = 500000.0
+
+
+# ------------------------------------------------------------------ the cases
+def listed():
+    return [
+        # one decode step of 16 users: rotate the fp32 rows that the q and k projections wrote
+        dict(name="rope_step", op="rope", T=16, hq=20, hk=5, D=128, rot=128, axes=1, inter=False,
+             src="f32", dst="bf16", far=8192),
+        # a long prompt's q and k
+        dict(name="rope_prompt", op="rope", T=8192, hq=20, hk=5, D=128, rot=128, axes=1,
+             inter=False, src="f32", dst="bf16", far=131072),
+        # patches of an image among text, three axes, bf16 rows
+        dict(name="rope_patches", op="rope", T=1521, hq=20, hk=5, D=128, rot=128, axes=3,
+             inter=False, src="bf16", dst="bf16", far=4096),
+        # one decode step of 24 users writes 24 rows of keys and values
+        dict(name="append_step", op="append", B=24, n=1, past=4000, hk=5, D=128, ps=64, src="f32"),
+        # four ragged prompts into an empty cache
+        dict(name="append_prompt", op="append", B=4, n=4099, past=0, hk=5, D=128, ps=64,
+             src="f32"),
+        # chunks of prompts behind cached text, heads of 64, small pages, bf16 rows
+        dict(name="append_chunk", op="append", B=7, n=333, past=517, hk=8, D=64, ps=16,
+             src="bf16"),
+        # one user, a short conversation: latency
+        dict(name="decode_one", op="decode", B=1, L=777, hk=5, rep=4, D=128, ps=64, window=0,
+             src="bf16"),
+        # 24 users with contexts of very different lengths
+        dict(name="decode_batch", op="decode", B=24, L=8191, hk=5, rep=4, D=128, ps=64, window=0,
+             src="bf16"),
+        # one user with a very long document
+        dict(name="decode_long", op="decode", B=1, L=262143, hk=5, rep=4, D=128, ps=64, window=0,
+             src="bf16"),
+        # a short prompt
+        dict(name="prefill_short", op="prefill", B=1, n=77, past=0, hk=5, rep=4, D=128, ps=64,
+             window=0, src="bf16"),
+        # two chunks of a long prompt behind what is cached already
+        dict(name="prefill_chunk", op="prefill", B=2, n=512, past=16000, hk=5, rep=4, D=128,
+             ps=64, window=0, src="bf16"),
+        # a long prompt in one go
+        dict(name="prefill_prompt", op="prefill", B=1, n=8192, past=0, hk=5, rep=4, D=128, ps=64,
+             window=0, src="bf16"),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    if hi <= lo:
+        return lo
+    return min(hi, max(lo, int(math.exp(rng.uniform(math.log(lo), math.log(hi + 1))))))
+
+
+def draw(rng):
+    op = rng.choice(["rope", "append", "decode", "prefill"])
+    D = rng.choice([64, 128])
+    hk = rng.choice([1, 2, 4, 5, 8])
+    rep = rng.choice([1, 2, 3, 4, 5, 8, 12, 16])
+    ps = rng.choice([16, 32, 64, 128])
+    src = rng.choice(["bf16", "f32"])
+    if op == "rope":
+        rot = rng.choice([D, D // 2])
+        cost = 8192 * 25 * 128
+        return dict(op=op, T=_log_int(rng, 1, cost // (hk * (rep + 1) * D)), hq=hk * rep, hk=hk,
+                    D=D, rot=rot, axes=rng.choice([1, 2, 3]), inter=rng.random() < 0.5, src=src,
+                    dst=rng.choice(["bf16", "f32"]), far=_log_int(rng, 1000, 1000000))
+    if op == "append":
+        B = _log_int(rng, 1, 64)
+        n = 1 if rng.random() < 0.4 else _log_int(rng, 1, 4 * 4099 * 5 * 128 // (hk * D * B))
+        return dict(op=op, B=B, n=n, past=rng.choice([0, _log_int(rng, 1, 4096)]), hk=hk, D=D,
+                    ps=ps, src=src)
+    if op == "decode":
+        B = _log_int(rng, 1, 128)
+        most = 262143 * 5 * 128 // (hk * D * B)
+        L = _log_int(rng, 16, min(131072, most))
+        window = rng.choice([0, 0, _log_int(rng, 1, L)])
+        return dict(op=op, B=B, L=L, hk=hk, rep=rep, D=D, ps=ps, window=window, src=src)
+    B = _log_int(rng, 1, 6)
+    area = 8192 * 8192 * 20 // (2 * hk * rep * B)
+    n = _log_int(rng, 2, min(8192, int(area ** 0.5)))
+    past = 0 if rng.random() < 0.5 else _log_int(rng, 1, min(32768, max(1, area // n - n)))
+    window = rng.choice([0, 0, _log_int(rng, 1, n + past)])
+    return dict(op=op, B=B, n=n, past=past, hk=hk, rep=rep, D=D, ps=ps, window=window, src=src)
+
+
+# ------------------------------------------------------------- host-side facts
+def _sections(case):
+    """Pairs turned by each axis: as equal as they can be, the first takes the rest."""
+    half, axes = case["rot"] // 2, case["axes"]
+    return [half - (axes - 1) * (half // axes)] + [half // axes] * (axes - 1)
+
+
+def _inv_freq(rot):
+    return (1.0 / THETA ** (np.arange(0, rot, 2, dtype=np.float64) / rot)).astype(np.float32)
+
+
+def _ragged(case):
+    """(new tokens, cached tokens with them) of every sequence: the case's own,
+    whatever the seed of its values."""
+    B = case["B"]
+    rng = np.random.default_rng([B, case.get("L", 0), case.get("n", 0), case.get("past", 0)])
+    if case["op"] == "decode":
+        lens = rng.integers(max(1, case["L"] // 8), case["L"] + 1, B)
+        lens[rng.integers(B)] = case["L"]
+        return np.ones(B, np.int64), lens
+    n = rng.integers(max(1, case["n"] // 2), case["n"] + 1, B)
+    n[rng.integers(B)] = case["n"]
+    past = rng.integers(case["past"] // 2, case["past"] + 1, B) if case["past"] else np.zeros(B, np.int64)
+    return n, past + n
+
+
+def _head_bytes(ps, D):
+    """One key/value head of a page: key codes, value codes, key scales, value scales."""
+    return ps * (D + 4)
+
+
+def _pairs(n, lens, window):
+    """Keys seen by all new tokens of a sequence: token i sits at lens - n + i."""
+    p = np.arange(int(lens) - int(n), int(lens), dtype=np.float64) + 1
+    p = np.maximum(p, 0)
+    return float(np.minimum(p, window).sum() if window else p.sum())
+
+
+def work(case):
+    c = case
+    size = {"bf16": 2, "f32": 4}
+    if c["op"] == "rope":
+        v = c["T"] * (c["hq"] + c["hk"]) * c["D"]
+        return {"bytes": v * (size[c["src"]] + size[c["dst"]]) + 4 * c["axes"] * c["T"] + 2 * c["rot"],
+                "flops": 3 * v * c["rot"] // c["D"]}
+    n, lens = _ragged(c)
+    row = c["hk"] * (c["D"] + 4)  # codes and scales of one token's keys and values
+    if c["op"] == "append":
+        v = int(n.sum()) * c["hk"] * c["D"] * 2
+        return {"bytes": v * size[c["src"]] + int(n.sum()) * row, "flops": 4 * v}
+    seen = np.minimum(lens, n - 1 + c["window"]) if c["window"] else lens
+    io = int(n.sum()) * c["hk"] * c["rep"] * (c["D"] * (size[c["src"]] + 2) + 4)
+    pairs = sum(_pairs(a, b, c["window"]) for a, b in zip(n, lens))
+    return {"bytes": int(seen.sum()) * row + io,
+            "flops": int(4 * pairs * c["D"] * c["hk"] * c["rep"])}
+
+
+# -------------------------------------------------------------------- the data
+def _views(pages, hk, ps, D):
+    """Key codes, value codes [pages, heads, ps, D/2], key and value scales
+    [pages, heads, ps] of a cache's pages."""
+    v = pages.view(pages.shape[0], hk, _head_bytes(ps, D))
+    c = ps * D // 2
+    sc = v[:, :, 2 * c:].view(torch.bfloat16)
+    return (v[:, :, :c].unflatten(-1, (ps, D // 2)), v[:, :, c:2 * c].unflatten(-1, (ps, D // 2)),
+            sc[:, :, :ps], sc[:, :, ps:])
+
+
+def _quantise(x):
+    """Codes + 8, two to a byte, and bf16 scales of rows [..., D]: the scale is
+    bf16(fl32(absmax / 7)), a code the nearest whole number to x / scale."""
+    seven = torch.full((), 7.0, device=x.device)
+    s = (x.float().abs().amax(-1) / seven.expand(x.shape[:-1])).bfloat16()
+    div = torch.where(s == 0, 1.0, s.double()).unsqueeze(-1)
+    code = (torch.round(x.double() / div) * (s != 0).unsqueeze(-1)).to(torch.int32) + 8
+    return (code[..., 0::2] | (code[..., 1::2] << 4)).to(torch.uint8), s
+
+
+def prepare(case, seed):
+    c = case
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device=DEV)
+
+    st = dict(case=c)
+    if c["op"] == "rope":
+        T = c["T"]
+        far = torch.tensor([c["far"]], device=DEV)
+        # text counts on along every axis; patches of an image count on their grid
+        start = int(torch.randint(0, max(1, c["far"] - T), (1,), generator=g, device=DEV))
+        pos = torch.arange(start, start + T, device=DEV).repeat(c["axes"], 1)
+        if c["axes"] > 1:
+            side = max(1, math.isqrt(T))
+            pos[1] = start + torch.arange(T, device=DEV) // side
+            pos[-1] = start + torch.arange(T, device=DEV) % side
+        st["pos"] = torch.minimum(pos, far).to(torch.int32).contiguous()
+        st["inv_freq"] = torch.from_numpy(_inv_freq(c["rot"])).to(DEV)
+        st["q"] = rand(T, c["hq"], c["D"]).to(dt[c["src"]])
+        st["k"] = rand(T, c["hk"], c["D"]).to(dt[c["src"]])
+        st["q_out"] = torch.empty_like(st["q"], dtype=dt[c["dst"]])
+        st["k_out"] = torch.empty_like(st["k"], dtype=dt[c["dst"]])
+        if own:
+            import ternary_absmax_int8_b200 as tq
+            st["rows"] = tq.make_rope_rows([
+                dict([("x_" + c["src"], st[n]), ("y_" + c["dst"], st[n + "_out"]),
+                      ("heads", c["h" + n])]) for n in ("q", "k")], head_dim=c["D"])
+        return st
+
+    n, lens = _ragged(c)
+    B, hk, D, ps = c["B"], c["hk"], c["D"], c["ps"]
+    need = -(-lens // ps)
+    width, total = int(need.max()), int(need.sum())
+    order = torch.randperm(total + 3, generator=g, device=DEV)[:total].cpu().numpy()
+    table = np.zeros((B, width), np.int32)
+    at = 0
+    for b in range(B):
+        table[b, :need[b]] = order[at:at + need[b]]
+        at += need[b]
+    st["table"] = torch.from_numpy(table).to(DEV)
+    st["lens"] = torch.from_numpy(lens.astype(np.int32)).to(DEV)
+    st["tok_start"] = torch.from_numpy(np.concatenate([[0], np.cumsum(n)]).astype(np.int32)).to(DEV)
+    T = int(n.sum())
+    st["T"] = T
+    pages = torch.zeros(total + 3, hk * _head_bytes(ps, D), dtype=torch.uint8, device=DEV)
+    kc, vc, ks, vs = _views(pages, hk, ps, D)
+    for code, scale, spread in ((kc, ks, 1.5), (vc, vs, 1.0)):
+        for p0 in range(0, pages.shape[0], 2048):  # a part at a time: less memory
+            x = rand(min(2048, pages.shape[0] - p0), hk, ps, D)
+            x *= spread * torch.exp(0.3 * rand(*x.shape[:3], 1))
+            code[p0:p0 + 2048], scale[p0:p0 + 2048] = _quantise(x)
+    st["pages"] = pages
+    if c["op"] == "append":
+        st["k"] = (1.5 * rand(T, hk, D)).to(dt[c["src"]])
+        st["v"] = rand(T, hk, D).to(dt[c["src"]])
+    else:
+        st["q"] = rand(T, hk * c["rep"], D).to(dt[c["src"]])
+        st["out"] = torch.empty(T, hk * c["rep"], D, dtype=torch.bfloat16, device=DEV)
+        st["lse"] = torch.empty(T, hk * c["rep"], device=DEV)
+    if own:
+        import ternary_absmax_int8_b200 as tq
+        st["cache"] = tq.make_kv4_cache(pages=pages, page_table=st["table"],
+                                        num_pages=pages.shape[0], page_size=ps, kv_heads=hk,
+                                        head_dim=D, batch=B, max_pages=width)
+        if c["op"] != "append":
+            size = (tq.tq_kv4_decode_workspace(st["cache"], hk * c["rep"]) if c["op"] == "decode"
+                    else tq.tq_kv4_prefill_workspace(st["cache"], hk * c["rep"], T))
+            st["workspace"] = torch.empty(max(16, size), dtype=torch.uint8, device=DEV)
+    return st
+
+
+# -------------------------------------------------------------- the plain forms
+def _plain_rope(st):
+    c = st["case"]
+    rot, half = c["rot"], c["rot"] // 2
+    axis = torch.repeat_interleave(torch.arange(c["axes"], device=DEV),
+                                   torch.tensor(_sections(c), device=DEV), output_size=half)
+    angle = st["pos"][axis].t().double() * st["inv_freq"].double()  # [T, half]
+    cos, sin = torch.cos(angle).float().unsqueeze(1), torch.sin(angle).float().unsqueeze(1)
+
+    def turn(x, out):
+        x = x.float()
+        y = x.clone()
+        i = slice(0, rot, 2) if c["inter"] else slice(0, half)
+        j = slice(1, rot, 2) if c["inter"] else slice(half, rot)
+        y[..., i] = x[..., i] * cos - x[..., j] * sin
+        y[..., j] = x[..., j] * cos + x[..., i] * sin
+        return y.to(out.dtype)
+
+    return {"q": turn(st["q"], st["q_out"]), "k": turn(st["k"], st["k_out"])}
+
+
+def _plain_append(st):
+    c = st["case"]
+    t = torch.arange(st["T"], device=DEV, dtype=torch.int32)
+    b = torch.searchsorted(st["tok_start"], t, right=True) - 1
+    pos = (st["lens"][b] - st["tok_start"][b + 1] + t).long()
+    page, slot = st["table"][b, pos // c["ps"]].long(), pos % c["ps"]
+    kc, vc, ks, vs = _views(st["pages"], c["hk"], c["ps"], c["D"])
+    kc[page, :, slot], ks[page, :, slot] = _quantise(st["k"])
+    vc[page, :, slot], vs[page, :, slot] = _quantise(st["v"])
+    return {"pages": st["pages"]}
+
+
+def _plain_attention(st):
+    c = st["case"]
+    B, hk, rep, D, ps = c["B"], c["hk"], c["rep"], c["D"], c["ps"]
+    L = st["table"].shape[1] * ps
+
+    def rows(code, scale):  # [B, hk, L, D]
+        x = code[st["table"].long()]  # [B, pages, hk, ps, D/2]
+        x = torch.stack([x & 15, x >> 4], -1).flatten(-2).float() - 8
+        x = x * scale[st["table"].long()].float().unsqueeze(-1)
+        return x.transpose(1, 2).reshape(B, hk, L, D)
+
+    kc, vc, ks, vs = _views(st["pages"], hk, ps, D)
+    start = st["tok_start"]
+    n = start[1:] - start[:-1]
+    N = c.get("n", 1)
+    i = torch.arange(N, device=DEV)
+    real = i < n.unsqueeze(1)  # [B, N]
+    token = torch.where(real, start[:-1].unsqueeze(1) + i, 0)
+    q = st["q"][token].float().view(B, N, hk, rep, D).permute(0, 2, 3, 1, 4)
+    s = q.reshape(B, hk, rep * N, D) @ rows(kc, ks).transpose(2, 3)
+    s = s.view(B, hk, rep, N, L) * (D ** -0.5)
+    p = ((st["lens"] - n).unsqueeze(1) + i).unsqueeze(-1)  # [B, N, 1]
+    j = torch.arange(L, device=DEV)
+    seen = j <= p
+    if c["window"]:
+        seen &= j > p - c["window"]
+    s.masked_fill_(~seen.view(B, 1, 1, N, L), -math.inf)
+    top = s.amax(-1, keepdim=True).clamp_min(torch.finfo(torch.float32).min)
+    s = s.sub_(top).exp_()
+    total = s.sum(-1, keepdim=True)
+    lse = (top + total.log()).squeeze(-1).permute(0, 3, 1, 2).reshape(B, N, hk * rep)
+    o = (s.view(B, hk, rep * N, L) @ rows(vc, vs)).view(B, hk, rep, N, D) / total.clamp_min(1e-30)
+    o = o.permute(0, 3, 1, 2, 4).reshape(B, N, hk * rep, D)
+    return {"out": o[real].bfloat16(), "lse": lse[real]}
+
+
+def run(state):
+    st, c = state, state["case"]
+    op = c["op"]
+    if not own:
+        return (_plain_rope(st) if op == "rope" else _plain_append(st) if op == "append"
+                else _plain_attention(st))
+    import ternary_absmax_int8_b200 as tq
+    if op == "rope":
+        tq.tq_rope(st["rows"], st["pos"], st["inv_freq"], _sections(c), c["T"], c["D"], c["rot"],
+                   flags=tq.TQ_ROPE_INTERLEAVED if c["inter"] else 0)
+        return {"q": st["q_out"], "k": st["k_out"]}
+    f32 = c["src"] == "f32"
+    if op == "append":
+        k, v = st["k"], st["v"]
+        tq.tq_kv4_append(st["cache"], None if f32 else k, None if f32 else v, k if f32 else None,
+                         v if f32 else None, st["tok_start"], st["lens"], st["T"])
+        return {"pages": st["pages"]}
+    q = st["q"]
+    if op == "decode":
+        tq.tq_kv4_decode(st["cache"], None if f32 else q, q if f32 else None, st["lens"],
+                         st["out"], st["lse"], c["hk"] * c["rep"], c["D"] ** -0.5, c["window"],
+                         st["workspace"], st["workspace"].numel())
+    else:
+        tq.tq_kv4_prefill(st["cache"], None if f32 else q, q if f32 else None, st["tok_start"],
+                          st["lens"], st["out"], st["lse"], st["T"], c["hk"] * c["rep"],
+                          c["D"] ** -0.5, c["window"], st["workspace"], st["workspace"].numel())
+    return {"out": st["out"], "lse": st["lse"]}
+
+
+# ------------------------------------------------- the definitions in 64 bits
+def _exact_rope(st):
+    c = st["case"]
+    pos, inv = st["pos"].cpu().numpy().astype(np.float64), st["inv_freq"].cpu().numpy()
+    half = c["rot"] // 2
+    angle, i0 = np.empty((c["T"], half)), 0
+    for a, count in enumerate(_sections(c)):
+        for i in range(i0, i0 + count):
+            angle[:, i] = pos[a] * np.float64(inv[i])
+        i0 += count
+    turn = torch.from_numpy(np.exp(1j * angle)).to(DEV).unsqueeze(1)  # a complex turn per pair
+    res = {}
+    for name in ("q", "k"):
+        x = st[name].double()
+        r = x[..., :c["rot"]]
+        z = (torch.view_as_complex(r.unflatten(-1, (half, 2)).contiguous()) if c["inter"]
+             else torch.complex(r[..., :half].contiguous(), r[..., half:].contiguous())) * turn
+        r = (torch.view_as_real(z).flatten(-2) if c["inter"] else torch.cat([z.real, z.imag], -1))
+        res[name] = torch.cat([r, x[..., c["rot"]:]], -1)
+    return res
+
+
+def _exact_append(st):
+    c = st["case"]
+    hk, D, ps = c["hk"], c["D"], c["ps"]
+    pages = st["pages"].cpu().numpy().copy()
+    start, lens, table = (st[k].cpu().numpy() for k in ("tok_start", "lens", "table"))
+    b = np.repeat(np.arange(c["B"]), np.diff(start))
+    pos = lens[b] - start[b + 1] + np.arange(st["T"])
+    page, slot = table[b, pos // ps], pos % ps
+    for which, name in enumerate(("k", "v")):
+        x = st[name].float().cpu().numpy()
+        bits = (np.abs(x).max(-1) / np.float32(7)).astype(np.float32).view(np.uint32).astype(np.uint64)
+        scale = ((bits + 0x7FFF + ((bits >> np.uint64(16)) & np.uint64(1))) >> np.uint64(16)).astype(np.uint32)
+        s64 = (scale << np.uint32(16)).view(np.float32).astype(np.float64)[..., None]
+        code = np.rint(np.divide(x.astype(np.float64), s64, out=np.zeros(x.shape), where=s64 > 0))
+        code = (code + 8).astype(np.uint8)
+        for h in range(hk):
+            o = h * _head_bytes(ps, D) + which * ps * D // 2 + slot * (D // 2)
+            at = o[:, None] + np.arange(D // 2)
+            pages[page[:, None], at] = code[:, h, 0::2] + 16 * code[:, h, 1::2]
+            o = h * _head_bytes(ps, D) + ps * D + which * ps * 2 + slot * 2
+            pages[page, o] = scale[:, h] & 255
+            pages[page, o + 1] = scale[:, h] >> 8
+    return {"pages": torch.from_numpy(pages)}
+
+
+def _exact_attention(st):
+    c = st["case"]
+    hk, rep, D, ps = c["hk"], c["rep"], c["D"], c["ps"]
+    # the two values of every byte
+    two = torch.tensor([[(v % 16) - 8, (v // 16) - 8] for v in range(256)], dtype=torch.float64,
+                       device=DEV)
+    start, lens = st["tok_start"].tolist(), st["lens"].tolist()
+    q = st["q"].double()
+    out = torch.zeros(q.shape, dtype=torch.float64, device=DEV)
+    lse = torch.full(q.shape[:2], -math.inf, dtype=torch.float64, device=DEV)
+    hb, cb = _head_bytes(ps, D), ps * D // 2
+    for b in range(c["B"]):
+        n, L = start[b + 1] - start[b], lens[b]
+        mine = st["pages"][st["table"][b, :-(-L // ps)].long()]
+        p = torch.arange(L - n, L, device=DEV).unsqueeze(1)
+        j = torch.arange(L, device=DEV)
+        off = (j > p) | (j <= p - (c["window"] or L + 1))
+        for h in range(hk):
+            blk = mine[:, h * hb:(h + 1) * hb]
+
+            def values(which):
+                code = two[blk[:, which * cb:(which + 1) * cb].long()].reshape(-1, D)[:L]
+                at = 2 * cb + which * 2 * ps
+                s = blk[:, at:at + 2 * ps].to(torch.int32)
+                s = ((s[:, 0::2] + 256 * s[:, 1::2]) * 65536).view(torch.float32)
+                return code * s.reshape(-1)[:L].double().unsqueeze(1)
+
+            k, v = values(0), values(1)
+            for r in range(h * rep, (h + 1) * rep):
+                s = (q[start[b]:start[b + 1], r] @ k.t()) / math.sqrt(D)
+                s[off] = -math.inf
+                z = torch.logsumexp(s, -1)
+                lse[start[b]:start[b + 1], r] = z
+                out[start[b]:start[b + 1], r] = torch.exp(s - z.unsqueeze(1)) @ v
+    return {"out": out, "lse": lse}
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    return {"rope": _exact_rope, "append": _exact_append, "decode": _exact_attention,
+            "prefill": _exact_attention}[case["op"]](st)
