@@ -38,23 +38,20 @@ def listed():
         dict(name="append_chunk", op="append", B=7, n=333, past=517, hk=8, D=64, ps=16,
              src="bf16"),
         # one user, a short conversation: latency
-        dict(name="decode_one", op="decode", B=1, L=777, hk=5, rep=4, D=128, ps=64, window=0,
-             src="bf16"),
+        dict(name="decode_one", op="decode", B=1, L=777, hk=5, rep=4, D=128, ps=64, window=0),
         # 24 users with contexts of very different lengths
-        dict(name="decode_batch", op="decode", B=24, L=8191, hk=5, rep=4, D=128, ps=64, window=0,
-             src="bf16"),
+        dict(name="decode_batch", op="decode", B=24, L=8191, hk=5, rep=4, D=128, ps=64, window=0),
         # one user with a very long document
-        dict(name="decode_long", op="decode", B=1, L=262143, hk=5, rep=4, D=128, ps=64, window=0,
-             src="bf16"),
+        dict(name="decode_long", op="decode", B=1, L=262143, hk=5, rep=4, D=128, ps=64, window=0),
         # a short prompt
         dict(name="prefill_short", op="prefill", B=1, n=77, past=0, hk=5, rep=4, D=128, ps=64,
-             window=0, src="bf16"),
+             window=0),
         # two chunks of a long prompt behind what is cached already
         dict(name="prefill_chunk", op="prefill", B=2, n=512, past=16000, hk=5, rep=4, D=128,
-             ps=64, window=0, src="bf16"),
+             ps=64, window=0),
         # a long prompt in one go
         dict(name="prefill_prompt", op="prefill", B=1, n=8192, past=0, hk=5, rep=4, D=128, ps=64,
-             window=0, src="bf16"),
+             window=0),
     ]
 
 
@@ -87,13 +84,13 @@ def draw(rng):
         most = 262143 * 5 * 128 // (hk * D * B)
         L = _log_int(rng, 16, min(131072, most))
         window = rng.choice([0, 0, _log_int(rng, 1, L)])
-        return dict(op=op, B=B, L=L, hk=hk, rep=rep, D=D, ps=ps, window=window, src=src)
+        return dict(op=op, B=B, L=L, hk=hk, rep=rep, D=D, ps=ps, window=window)
     B = _log_int(rng, 1, 6)
     area = 8192 * 8192 * 20 // (2 * hk * rep * B)
     n = _log_int(rng, 2, min(8192, int(area ** 0.5)))
     past = 0 if rng.random() < 0.5 else _log_int(rng, 1, min(32768, max(1, area // n - n)))
     window = rng.choice([0, 0, _log_int(rng, 1, n + past)])
-    return dict(op=op, B=B, n=n, past=past, hk=hk, rep=rep, D=D, ps=ps, window=window, src=src)
+    return dict(op=op, B=B, n=n, past=past, hk=hk, rep=rep, D=D, ps=ps, window=window)
 
 
 # ------------------------------------------------------------- host-side facts
@@ -147,7 +144,7 @@ def work(case):
         v = int(n.sum()) * c["hk"] * c["D"] * 2
         return {"bytes": v * size[c["src"]] + int(n.sum()) * row, "flops": 4 * v}
     seen = np.minimum(lens, n - 1 + c["window"]) if c["window"] else lens
-    io = int(n.sum()) * c["hk"] * c["rep"] * (c["D"] * (size[c["src"]] + 2) + 4)
+    io = int(n.sum()) * c["hk"] * c["rep"] * (c["D"] * 4 + 4)
     pairs = sum(_pairs(a, b, c["window"]) for a, b in zip(n, lens))
     return {"bytes": int(seen.sum()) * row + io,
             "flops": int(4 * pairs * c["D"] * c["hk"] * c["rep"])}
@@ -233,7 +230,7 @@ def prepare(case, seed):
         st["k"] = (1.5 * rand(T, hk, D)).to(dt[c["src"]])
         st["v"] = rand(T, hk, D).to(dt[c["src"]])
     else:
-        st["q"] = rand(T, hk * c["rep"], D).to(dt[c["src"]])
+        st["q"] = rand(T, hk * c["rep"], D).bfloat16()
         st["out"] = torch.empty(T, hk * c["rep"], D, dtype=torch.bfloat16, device=DEV)
         st["lse"] = torch.empty(T, hk * c["rep"], device=DEV)
     if own:
@@ -328,21 +325,19 @@ def run(state):
         tq.tq_rope(st["rows"], st["pos"], st["inv_freq"], _sections(c), c["T"], c["D"], c["rot"],
                    flags=tq.TQ_ROPE_INTERLEAVED if c["inter"] else 0)
         return {"q": st["q_out"], "k": st["k_out"]}
-    f32 = c["src"] == "f32"
     if op == "append":
-        k, v = st["k"], st["v"]
+        k, v, f32 = st["k"], st["v"], c["src"] == "f32"
         tq.tq_kv4_append(st["cache"], None if f32 else k, None if f32 else v, k if f32 else None,
                          v if f32 else None, st["tok_start"], st["lens"], st["T"])
         return {"pages": st["pages"]}
-    q = st["q"]
     if op == "decode":
-        tq.tq_kv4_decode(st["cache"], None if f32 else q, q if f32 else None, st["lens"],
-                         st["out"], st["lse"], c["hk"] * c["rep"], c["D"] ** -0.5, c["window"],
-                         st["workspace"], st["workspace"].numel())
+        tq.tq_kv4_decode(st["cache"], st["q"], st["lens"], st["out"], st["lse"],
+                         c["hk"] * c["rep"], c["D"] ** -0.5, c["window"], st["workspace"],
+                         st["workspace"].numel())
     else:
-        tq.tq_kv4_prefill(st["cache"], None if f32 else q, q if f32 else None, st["tok_start"],
-                          st["lens"], st["out"], st["lse"], st["T"], c["hk"] * c["rep"],
-                          c["D"] ** -0.5, c["window"], st["workspace"], st["workspace"].numel())
+        tq.tq_kv4_prefill(st["cache"], st["q"], st["tok_start"], st["lens"], st["out"], st["lse"],
+                          st["T"], c["hk"] * c["rep"], c["D"] ** -0.5, c["window"],
+                          st["workspace"], st["workspace"].numel())
     return {"out": st["out"], "lse": st["lse"]}
 
 
