@@ -426,6 +426,166 @@ tq_status tq_gemv_binary_stack(const tq_binary_proj *projs, int n_proj, int M,
                                cudaStream_t stream);
 
 /*
+ * tq_rope -- rotary positions of query and key rows, with one to four axes
+ * (text counts along one; image and video patches along time, height and
+ * width). No page prints the formula; the model the projections belong to is
+ * a Llama variant (lemon-mlx-engine issue, section "Architecture"; its check
+ * list names RoPE). Reading: the first rot_dim values of each head are
+ * rot_dim / 2 pairs, (i, i + rot_dim/2) or, with TQ_ROPE_INTERLEAVED,
+ * (2i, 2i + 1); pair i belongs to the axis whose section holds i and turns by
+ *   angle = pos[axis, t] * inv_freq[i]        (fp64, reduced in fp64)
+ *   (u, v) -> (u cos - v sin, v cos + u sin)  (fp32, rounded once to y's type)
+ * and the values behind rot_dim are copied.
+ *   rows      HOST array of n entries (read during the call only), 0 <= n <= 4:
+ *             typically the q and the k rows of a layer, in one launch.
+ *   pos       device, int32 [n_axes, T], rows pos_stride entries apart
+ *   inv_freq  device, fp32 [rot_dim / 2] (scaled frequencies are the caller's)
+ *   sections  HOST, n_axes counts of pairs, in order; their sum is rot_dim / 2
+ * head_dim % 8 == 0, head_dim <= 1024; rot_dim % 16 == 0, 0 <= rot_dim <= head_dim;
+ * 1 <= n_axes <= 4 (TQ_ERR_SHAPE). x and y 16-byte aligned and strides whole
+ * 16-byte multiples (TQ_ERR_ALIGN). y may be x itself (same type, same
+ * stride); no other overlap. T == 0 is a no-op. Asynchronous; waits for the
+ * previous kernel on the stream before it touches memory.
+ */
+#define TQ_ROPE_INTERLEAVED 1u
+
+typedef struct tq_rope_rows {
+    const uint16_t *x_bf16;   /* device [T, heads, head_dim]: exactly one of */
+    const float *x_f32;       /* x_bf16 and x_f32 is not NULL */
+    uint16_t *y_bf16;         /* device [T, heads, head_dim]: exactly one of */
+    float *y_f32;             /* y_bf16 and y_f32 is not NULL */
+    int64_t x_stride;         /* values from one token to the next; 0: heads * head_dim */
+    int64_t y_stride;
+    int heads;                /* >= 0; 0: nothing to do */
+    int reserved;             /* set to 0 */
+} tq_rope_rows;
+
+tq_status tq_rope(const tq_rope_rows *rows, int n, const int32_t *pos, int64_t pos_stride,
+                  const float *inv_freq, const int *sections, int n_axes, int T, int head_dim,
+                  int rot_dim, unsigned flags, cudaStream_t stream);
+
+/*
+ * The 4-bit key/value cache: what stands between the q, k, v projections and
+ * o_proj, at a quarter of a 16-bit cache's bytes (decode at long contexts is
+ * bound by them as it is by the weights: 1bit engine blog, "Qwen3.8-27B at
+ * 45.7 tok/s ..."). No page gives a format; this one follows the activations:
+ * absmax per token, here per token and key/value head.
+ *   s = bf16(fl32(absmax / 7));  code = the whole number nearest to x / s
+ *   (ties to even, decided exactly), -7..7;  value = code * s.
+ *   A row of zeros (or one whose s rounds to 0) has s = 0 and codes 0. A row
+ *   that holds a NaN or an infinity has s = NaN and codes 0: attention that
+ *   sees it gives NaN, attention that does not is unharmed.
+ * The cache is a set of pages of page_size tokens. A page holds, for each
+ * key/value head in turn, one block of page_size * (head_dim + 4) bytes:
+ *   key codes    [page_size, head_dim / 2], code + 8 in 4 bits, element 2i in
+ *                the low half of byte i
+ *   value codes  [page_size, head_dim / 2]
+ *   key scales   bf16 [page_size]
+ *   value scales bf16 [page_size]
+ * Token j of sequence b lives in page page_table[b, j / page_size] at slot
+ * j % page_size. Pages are the caller's to hand out, share and copy.
+ *
+ * Lengths and tables are device memory, so the calls can be captured in a
+ * graph and replayed as sequences grow. The kernels check them: a length
+ * beyond max_pages * page_size, or a page index outside [0, num_pages) that a
+ * call needs, sets bit 2 of the device error word (tq_device_error); nothing
+ * outside the pages is read or written, the length is cut, the page's keys
+ * are skipped (its new tokens dropped). Negative lengths count as 0.
+ */
+typedef struct tq_kv4_cache {
+    uint8_t *pages;            /* device, 16-byte aligned */
+    const int32_t *page_table; /* device [batch, max_pages] */
+    int64_t page_stride;       /* bytes from one page to the next: a multiple of 16, at
+                                  least tq_kv4_page_bytes; 0: tq_kv4_page_bytes */
+    int num_pages;
+    int page_size;             /* tokens: 16, 32, 64 or 128 */
+    int kv_heads;
+    int head_dim;              /* 64 or 128 */
+    int batch;                 /* sequences */
+    int max_pages;             /* entries of a table row; max_pages * page_size < 2^30 */
+} tq_kv4_cache;
+
+/* Bytes of one page (0 for a shape the cache does not take). */
+size_t tq_kv4_page_bytes(int page_size, int kv_heads, int head_dim);
+
+/*
+ * tq_kv4_append -- quantise new tokens' keys and values into their pages.
+ *   k, v      device rows [T, kv_heads, head_dim], both bf16 or both fp32
+ *             (the projections' own outputs): exactly one pair is not NULL.
+ *             k_stride, v_stride: values from one token to the next, 0:
+ *             kv_heads * head_dim; rows 16-byte aligned.
+ *   tok_start device int32 [batch + 1], non-decreasing: sequence b's new
+ *             tokens are rows tok_start[b] .. tok_start[b+1] - 1 (none where
+ *             equal); rows outside [tok_start[0], tok_start[batch]) are
+ *             padding and ignored. NULL: T == batch and row b is sequence b's
+ *             one new token.
+ *   lens      device int32 [batch]: cached tokens of each sequence WITH the
+ *             new ones; a sequence's n new tokens take positions lens - n ..
+ *             lens - 1. Tokens with a negative position are dropped (a
+ *             sequence of length 0 in a padded batch).
+ * Two tokens of one call must not share a slot (tables that name one page
+ * twice where both write). One launch; waits for the previous kernel on the
+ * stream before it touches memory.
+ */
+tq_status tq_kv4_append(const tq_kv4_cache *cache, const uint16_t *k_bf16,
+                        const uint16_t *v_bf16, const float *k_f32, const float *v_f32,
+                        int64_t k_stride, int64_t v_stride, const int32_t *tok_start,
+                        const int32_t *lens, int T, cudaStream_t stream);
+
+/*
+ * Attention over the cache. Query head h reads key/value head
+ * h / (q_heads / kv_heads). The query of a token at position p sees the keys
+ * j <= p, j > p - window where window > 0:
+ *   z_j = scale * (q . k_j),  out = sum_j softmax(z)_j v_j,
+ *   lse = log(sum_j exp(z_j))   (natural logarithm)
+ * A query that sees nothing has out = 0 and lse = -infinity. q . codes is an
+ * fp32 sum: query values are finite and at most 2^117 in magnitude, else the
+ * rows of that head and token may be NaN.
+ */
+typedef struct tq_kv4_query {
+    const uint16_t *q;       /* device, bf16 [T, q_heads, head_dim], 16-byte aligned (tq_rope
+                                writes it from the projection's fp32 rows) */
+    uint16_t *out;           /* device, bf16 [T, q_heads, head_dim], written, 16-byte aligned */
+    float *lse;              /* device, fp32 [T, q_heads], written; NULL: not wanted */
+    int64_t q_stride;        /* values from one token to the next (a multiple of 16 bytes); */
+    int64_t out_stride;      /* 0: q_heads * head_dim */
+    int q_heads;             /* a multiple of kv_heads, at most 64 times as many */
+    int window;              /* >= 0; 0: no window */
+    float scale;             /* > 0, finite */
+    int reserved;            /* set to 0 */
+} tq_kv4_query;
+
+/*
+ * tq_kv4_decode -- one new token per sequence: row b of q and out is sequence
+ * b's query, at position lens[b] - 1 (append it first).
+ *   workspace  device, 16-byte aligned, tq_kv4_decode_workspace bytes: partial
+ *              results of sequences split over several SMs. Its contents do
+ *              not matter before or after a call; calls that may overlap on
+ *              the GPU (two streams, two graphs replayed at once) need one
+ *              each.
+ * Results do not depend on the order in which SMs finish: the same inputs
+ * give the same bits on every run.
+ */
+tq_status tq_kv4_decode(const tq_kv4_cache *cache, const tq_kv4_query *query,
+                        const int32_t *lens, void *workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+
+/*
+ * tq_kv4_prefill -- any number of new tokens per sequence (prompts, chunks of
+ * prompts behind cached text, drafts to be verified): T rows of q and out,
+ * tok_start as in tq_kv4_append (required). Rows outside [tok_start[0],
+ * tok_start[batch]) are neither read nor written.
+ *   workspace  as in tq_kv4_decode, tq_kv4_prefill_workspace bytes for T rows.
+ */
+tq_status tq_kv4_prefill(const tq_kv4_cache *cache, const tq_kv4_query *query,
+                         const int32_t *tok_start, const int32_t *lens, int T, void *workspace,
+                         size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes for the current device (0 is possible: NULL will do then). */
+tq_status tq_kv4_decode_workspace(const tq_kv4_cache *cache, int q_heads, size_t *bytes);
+tq_status tq_kv4_prefill_workspace(const tq_kv4_cache *cache, int q_heads, int T, size_t *bytes);
+
+/*
  * tq_selftest_wait_timeout -- exercise the failure path of the kernels'
  * bounded waits without a fault: one thread waits, with the same bounded
  * wait the kernels use, on an mbarrier that nothing ever arrives on. After
@@ -439,8 +599,9 @@ tq_status tq_selftest_wait_timeout(unsigned limit_us, cudaStream_t stream);
  * tq_device_error -- read (and if reset != 0, clear) the library's device
  * error word on the current device. Synchronises the device. 0 means no
  * kernel has reported an error. A nonzero value means a kernel gave up a
- * bounded wait (its outputs are then invalid); bits: 1 = pipeline wait timed
- * out.
+ * bounded wait or met a bad index (its outputs are then invalid); bits: 1 =
+ * pipeline wait timed out; 2 = a page index or a length outside the key/value
+ * cache.
  */
 tq_status tq_device_error(uint32_t *code, int reset);
 

@@ -25,6 +25,9 @@ __all__ = [
     "tq_hadamard_quantize_act", "tq_hadamard_quantize_act_stack", "TqBinaryProj",
     "tq_pack_binary_host", "tq_gemv_binary",
     "tq_gemv_binary_stack", "make_binary_proj",
+    "TQ_ROPE_INTERLEAVED", "TqRopeRows", "make_rope_rows", "tq_rope",
+    "TqKv4Cache", "TqKv4Query", "make_kv4_cache", "tq_kv4_page_bytes", "tq_kv4_append",
+    "tq_kv4_decode_workspace", "tq_kv4_prefill_workspace", "tq_kv4_decode", "tq_kv4_prefill",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -34,6 +37,7 @@ TQ_STACK_OVERLAP_PREV = 1
 TQ_STACK_QUANTIZE = 2
 TQ_STACK_RMSNORM = 4
 TQ_STACK_RELU2_MUL = 8
+TQ_ROPE_INTERLEAVED = 1
 _STATUS = {0: "TQ_OK", 1: "TQ_ERR_NULL", 2: "TQ_ERR_SHAPE", 3: "TQ_ERR_ALIGN",
            4: "TQ_ERR_VALUE", 5: "TQ_ERR_CUDA", 6: "TQ_ERR_UNSUPPORTED"}
 
@@ -83,6 +87,51 @@ class TqBinaryProj(ctypes.Structure):
     ]
 
 
+class TqRopeRows(ctypes.Structure):
+    """Mirror of ``struct tq_rope_rows``."""
+    _fields_ = [
+        ("x_bf16", ctypes.c_void_p),
+        ("x_f32", ctypes.c_void_p),
+        ("y_bf16", ctypes.c_void_p),
+        ("y_f32", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64),
+        ("y_stride", ctypes.c_int64),
+        ("heads", ctypes.c_int),
+        ("reserved", ctypes.c_int),
+    ]
+
+
+class TqKv4Cache(ctypes.Structure):
+    """Mirror of ``struct tq_kv4_cache``."""
+    _fields_ = [
+        ("pages", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("num_pages", ctypes.c_int),
+        ("page_size", ctypes.c_int),
+        ("kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("batch", ctypes.c_int),
+        ("max_pages", ctypes.c_int),
+    ]
+
+
+class TqKv4Query(ctypes.Structure):
+    """Mirror of ``struct tq_kv4_query``."""
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+        ("q_heads", ctypes.c_int),
+        ("window", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_int),
+    ]
+
+
+_i64, _sz = ctypes.c_int64, ctypes.c_size_t
 _SIGS = {
     "tq_pack_host": [_vp, _vp, _i, _i, _i, _vp],
     "tq_quantize_act": [_vp, _vp, _vp, _vp, _i, _i, _i, _vp],
@@ -104,6 +153,15 @@ _SIGS = {
     "tq_pack_binary_host": [_vp, _vp, _vp, _vp, _i, _i],
     "tq_gemv_binary": [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp],
     "tq_gemv_binary_stack": [ctypes.POINTER(TqBinaryProj), _i, _i, _vp],
+    "tq_rope": [ctypes.POINTER(TqRopeRows), _i, _vp, _i64, _vp, ctypes.POINTER(_i), _i, _i, _i,
+                _i, ctypes.c_uint, _vp],
+    "tq_kv4_append": [ctypes.POINTER(TqKv4Cache), _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _i,
+                      _vp],
+    "tq_kv4_decode": [ctypes.POINTER(TqKv4Cache), ctypes.POINTER(TqKv4Query), _vp, _vp, _sz, _vp],
+    "tq_kv4_prefill": [ctypes.POINTER(TqKv4Cache), ctypes.POINTER(TqKv4Query), _vp, _vp, _i, _vp,
+                       _sz, _vp],
+    "tq_kv4_decode_workspace": [ctypes.POINTER(TqKv4Cache), _i, ctypes.POINTER(_sz)],
+    "tq_kv4_prefill_workspace": [ctypes.POINTER(TqKv4Cache), _i, _i, ctypes.POINTER(_sz)],
 }
 _lib_handle = None
 
@@ -123,6 +181,8 @@ def _load():
             fn.restype = ctypes.c_int
         lib.tq_status_string.argtypes = [ctypes.c_int]
         lib.tq_status_string.restype = ctypes.c_char_p
+        lib.tq_kv4_page_bytes.argtypes = [_i, _i, _i]
+        lib.tq_kv4_page_bytes.restype = _sz
         lib.tq_last_error.argtypes = []
         lib.tq_last_error.restype = ctypes.c_char_p
         _lib_handle = lib
@@ -299,3 +359,98 @@ def tq_device_error(reset: bool = False) -> int:
     code = ctypes.c_uint32(0)
     _check(_load().tq_device_error(ctypes.byref(code), 1 if reset else 0))
     return int(code.value)
+
+
+def _gpu_ptr(t, size: int):
+    """Pointer of a device tensor of `size`-byte elements on the current device (an int or
+    None passes through); a tensor elsewhere is refused, as the kernel would run here."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if t.element_size() != size:
+        raise TQError(4, f"a tensor of {size}-byte elements is wanted, not {t.dtype}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise TQError(4, f"a tensor on {t.device}: tensors must be on the current CUDA device")
+    return t.data_ptr()
+
+
+def make_rope_rows(rows, head_dim: int):
+    """A table of ``tq_rope_rows`` from dicts with the keys x_bf16 or x_f32, y_bf16 or y_f32,
+    heads and, for rows that are not packed, x_stride and y_stride (values between tokens)."""
+    arr = (TqRopeRows * len(rows))()
+    for e, r in zip(arr, rows):
+        e.x_bf16, e.x_f32 = _gpu_ptr(r.get("x_bf16"), 2), _gpu_ptr(r.get("x_f32"), 4)
+        e.y_bf16, e.y_f32 = _gpu_ptr(r.get("y_bf16"), 2), _gpu_ptr(r.get("y_f32"), 4)
+        e.heads = int(r["heads"])
+        e.x_stride = int(r.get("x_stride", 0)) or e.heads * int(head_dim)
+        e.y_stride = int(r.get("y_stride", 0)) or e.heads * int(head_dim)
+    return arr
+
+
+def tq_rope(rows, pos, inv_freq, sections, T: int, head_dim: int, rot_dim: int, flags: int = 0,
+            pos_stride: int = 0, stream=None) -> None:
+    """Rotary positions of the rows in a make_rope_rows table; pos int32 [len(sections), T]."""
+    n = len(sections)
+    _check(_load().tq_rope(rows, len(rows), _gpu_ptr(pos, 4), int(pos_stride) or int(T),
+                           _gpu_ptr(inv_freq, 4), (_i * n)(*sections), n, int(T), int(head_dim),
+                           int(rot_dim), int(flags), _stream(stream)))
+
+
+def tq_kv4_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
+    return _load().tq_kv4_page_bytes(int(page_size), int(kv_heads), int(head_dim))
+
+
+def make_kv4_cache(pages=None, page_table=None, num_pages: int = 0, page_size: int = 64,
+                   kv_heads: int = 1, head_dim: int = 128, batch: int = 0, max_pages: int = 0,
+                   page_stride: int = 0) -> TqKv4Cache:
+    """Describe a 4-bit key/value cache. It holds pointers only: keep the tensors."""
+    return TqKv4Cache(_gpu_ptr(pages, 1), _gpu_ptr(page_table, 4), int(page_stride),
+                      int(num_pages), int(page_size), int(kv_heads), int(head_dim), int(batch),
+                      int(max_pages))
+
+
+def tq_kv4_append(cache, k_bf16, v_bf16, k_f32, v_f32, tok_start, lens, T: int, k_stride: int = 0,
+                  v_stride: int = 0, stream=None) -> None:
+    """Quantise new keys and values into the cache's pages (one of the two pairs)."""
+    _check(_load().tq_kv4_append(ctypes.byref(cache), _gpu_ptr(k_bf16, 2), _gpu_ptr(v_bf16, 2),
+                                 _gpu_ptr(k_f32, 4), _gpu_ptr(v_f32, 4), int(k_stride),
+                                 int(v_stride), _gpu_ptr(tok_start, 4), _gpu_ptr(lens, 4), int(T),
+                                 _stream(stream)))
+
+
+def tq_kv4_decode_workspace(cache, q_heads: int) -> int:
+    size = _sz(0)
+    _check(_load().tq_kv4_decode_workspace(ctypes.byref(cache), int(q_heads), ctypes.byref(size)))
+    return size.value
+
+
+def tq_kv4_prefill_workspace(cache, q_heads: int, T: int) -> int:
+    size = _sz(0)
+    _check(_load().tq_kv4_prefill_workspace(ctypes.byref(cache), int(q_heads), int(T),
+                                            ctypes.byref(size)))
+    return size.value
+
+
+def _kv4_query(q, out, lse, q_heads, scale, window, q_stride, out_stride):
+    return ctypes.byref(TqKv4Query(_gpu_ptr(q, 2), _gpu_ptr(out, 2), _gpu_ptr(lse, 4),
+                                   int(q_stride), int(out_stride), int(q_heads),
+                                   int(window), float(scale), 0))
+
+
+def tq_kv4_decode(cache, q, lens, out, lse, q_heads: int, scale: float, window: int = 0,
+                  workspace=None, workspace_bytes: int = 0, q_stride: int = 0,
+                  out_stride: int = 0, stream=None) -> None:
+    """Attention of one new token per sequence over the cache."""
+    query = _kv4_query(q, out, lse, q_heads, scale, window, q_stride, out_stride)
+    _check(_load().tq_kv4_decode(ctypes.byref(cache), query, _gpu_ptr(lens, 4),
+                                 _gpu_ptr(workspace, 1), int(workspace_bytes), _stream(stream)))
+
+
+def tq_kv4_prefill(cache, q, tok_start, lens, out, lse, T: int, q_heads: int, scale: float,
+                   window: int = 0, workspace=None, workspace_bytes: int = 0, q_stride: int = 0,
+                   out_stride: int = 0, stream=None) -> None:
+    """Attention of any number of new tokens per sequence over the cache."""
+    query = _kv4_query(q, out, lse, q_heads, scale, window, q_stride, out_stride)
+    _check(_load().tq_kv4_prefill(ctypes.byref(cache), query, _gpu_ptr(tok_start, 4),
+                                  _gpu_ptr(lens, 4), int(T), _gpu_ptr(workspace, 1),
+                                  int(workspace_bytes), _stream(stream)))

@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "tq.h"
+#include "kv4_common.cuh"
 #include "tq_internal.h"
 
 namespace tq {
@@ -409,9 +410,328 @@ tq_status gemv_stack_impl(const char *fname, const tq_proj *projs, int n_proj, i
     return ok();
 }
 
+// Checks of a cache description; with at least one sequence the pointers too.
+tq_status check_kv4_cache(const char *fn, const tq_kv4_cache *c, tq::Kv4View *view)
+{
+    if (!c)
+        return fail(TQ_ERR_NULL, "%s: cache is NULL", fn);
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+        return fail(TQ_ERR_SHAPE, "%s: page_size=%d is not 16, 32, 64 or 128", fn, c->page_size);
+    if (c->head_dim != 64 && c->head_dim != 128)
+        return fail(TQ_ERR_UNSUPPORTED, "%s: head_dim=%d is not 64 or 128", fn, c->head_dim);
+    if (c->kv_heads < 1 || c->kv_heads > 1024)
+        return fail(TQ_ERR_SHAPE, "%s: kv_heads=%d is not in 1..1024", fn, c->kv_heads);
+    if (c->batch < 0 || c->num_pages < 0 || c->max_pages < 0)
+        return fail(TQ_ERR_SHAPE, "%s: negative size (batch=%d num_pages=%d max_pages=%d)", fn,
+                    c->batch, c->num_pages, c->max_pages);
+    if (c->batch > 65536)
+        return fail(TQ_ERR_UNSUPPORTED, "%s: batch=%d exceeds 65536", fn, c->batch);
+    if ((long long)c->max_pages * c->page_size >= (1ll << 30))
+        return fail(TQ_ERR_UNSUPPORTED, "%s: max_pages=%d pages of %d tokens", fn, c->max_pages,
+                    c->page_size);
+    const long long bytes =
+        (long long)tq_kv4_page_bytes(c->page_size, c->kv_heads, c->head_dim);
+    if (c->page_stride != 0 && c->page_stride < bytes)
+        return fail(TQ_ERR_SHAPE, "%s: page_stride=%lld is less than a page's %lld bytes", fn,
+                    (long long)c->page_stride, bytes);
+    if (c->page_stride % 16 != 0)
+        return fail(TQ_ERR_ALIGN, "%s: page_stride=%lld is not a multiple of 16", fn,
+                    (long long)c->page_stride);
+    if (c->batch > 0 && c->max_pages > 0) {
+        if (!c->page_table || (c->num_pages > 0 && !c->pages))
+            return fail(TQ_ERR_NULL, "%s: the cache's pages or page_table is NULL", fn);
+        if (!aligned(c->pages, 16) || !aligned(c->page_table, 4))
+            return fail(TQ_ERR_ALIGN, "%s: pages must be 16-byte, page_table 4-byte aligned", fn);
+    }
+    view->pages = c->pages;
+    view->table = c->page_table;
+    view->page_stride = c->page_stride ? c->page_stride : bytes;
+    view->num_pages = c->num_pages;
+    view->max_pages = c->max_pages;
+    view->batch = c->batch;
+    view->kv_heads = c->kv_heads;
+    view->lg_ps = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
+    return TQ_OK;
+}
+
+// The device's error word, which the cache's kernels need.
+tq_status kv4_error_word(const char *fn, tq::Kv4View *view)
+{
+    view->err = tq::device_error_word();
+    return view->err ? TQ_OK : fail(TQ_ERR_CUDA, "%s: no device error word", fn);
+}
+
+// The distance between rows of `heads` heads: 0 stands for packed rows.
+tq_status check_rows(const char *fn, const char *what, const void *p, long long stride,
+                     long long packed, int esize, long long *out)
+{
+    if (!aligned(p, 16) || (stride * esize) % 16 != 0)
+        return fail(TQ_ERR_ALIGN, "%s: %s must be 16-byte aligned, its stride a multiple of 16 "
+                    "bytes", fn, what);
+    if (stride != 0 && stride < packed)
+        return fail(TQ_ERR_SHAPE, "%s: %s: stride %lld is less than a row's %lld values", fn, what,
+                    stride, packed);
+    *out = stride ? stride : packed;
+    return TQ_OK;
+}
+
+tq_status check_kv4_heads(const char *fn, const tq_kv4_cache *c, int q_heads)
+{
+    if (q_heads < 1 || q_heads % c->kv_heads != 0)
+        return fail(TQ_ERR_SHAPE, "%s: q_heads=%d is not a multiple of kv_heads=%d", fn, q_heads,
+                    c->kv_heads);
+    if (q_heads / c->kv_heads > tq::kKv4MaxGroup)
+        return fail(TQ_ERR_UNSUPPORTED, "%s: %d query heads per key/value head (at most %d)", fn,
+                    q_heads / c->kv_heads, tq::kKv4MaxGroup);
+    return TQ_OK;
+}
+
+tq_status check_kv4_query(const char *fn, const tq_kv4_cache *c, const tq_kv4_query *q,
+                          tq::Kv4Query *out)
+{
+    if (!q)
+        return fail(TQ_ERR_NULL, "%s: query is NULL", fn);
+    tq_status st = check_kv4_heads(fn, c, q->q_heads);
+    if (st != TQ_OK)
+        return st;
+    if (!(q->scale > 0.0f) || q->scale > FLT_MAX)
+        return fail(TQ_ERR_VALUE, "%s: scale must be finite and > 0", fn);
+    if (q->window < 0)
+        return fail(TQ_ERR_VALUE, "%s: window=%d is negative", fn, q->window);
+    if (!q->q || !q->out)
+        return fail(TQ_ERR_NULL, "%s: q or out is NULL", fn);
+    if (q->lse && !aligned(q->lse, 4))
+        return fail(TQ_ERR_ALIGN, "%s: lse must be 4-byte aligned", fn);
+    const long long packed = (long long)q->q_heads * c->head_dim;
+    *out = tq::Kv4Query{q->q, q->out, q->lse, 0, 0, q->q_heads, q->window, q->scale};
+    st = check_rows(fn, "q", q->q, q->q_stride, packed, 2, &out->q_stride);
+    return st != TQ_OK ? st
+                       : check_rows(fn, "out", q->out, q->out_stride, packed, 2, &out->out_stride);
+}
+
+tq_status check_workspace(const char *fn, const void *p, size_t have, size_t need)
+{
+    if (need == 0)
+        return TQ_OK;
+    if (!p)
+        return fail(TQ_ERR_NULL, "%s: workspace is NULL", fn);
+    if (!aligned(p, 16))
+        return fail(TQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+    if (have < need)
+        return fail(TQ_ERR_SHAPE, "%s: workspace of %zu bytes, %zu are needed", fn, have, need);
+    return TQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+tq_status tq_rope(const tq_rope_rows *rows, int n, const int32_t *pos, int64_t pos_stride,
+                  const float *inv_freq, const int *sections, int n_axes, int T, int head_dim,
+                  int rot_dim, unsigned flags, cudaStream_t stream)
+{
+    const char *fn = "tq_rope";
+    if (n < 0 || n > tq::kRopeMaxRows || T < 0)
+        return fail(TQ_ERR_SHAPE, "%s: n=%d (0..%d) T=%d", fn, n, tq::kRopeMaxRows, T);
+    if (head_dim < 8 || head_dim > 1024 || head_dim % 8 != 0)
+        return fail(TQ_ERR_SHAPE, "%s: head_dim=%d is not a multiple of 8 in 8..1024", fn, head_dim);
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0)
+        return fail(TQ_ERR_SHAPE, "%s: rot_dim=%d is not a multiple of 16 in 0..head_dim", fn,
+                    rot_dim);
+    if (n_axes < 1 || n_axes > tq::kRopeMaxAxes)
+        return fail(TQ_ERR_SHAPE, "%s: n_axes=%d is not in 1..%d", fn, n_axes, tq::kRopeMaxAxes);
+    if (flags & ~TQ_ROPE_INTERLEAVED)
+        return fail(TQ_ERR_VALUE, "%s: bad flags 0x%x", fn, flags);
+    if (!sections)
+        return fail(TQ_ERR_NULL, "%s: sections is NULL", fn);
+    long long pairs = 0;
+    for (int a = 0; a < n_axes; ++a) {
+        if (sections[a] < 0)
+            return fail(TQ_ERR_SHAPE, "%s: sections[%d]=%d", fn, a, sections[a]);
+        pairs += sections[a];
+    }
+    if (pairs != rot_dim / 2)
+        return fail(TQ_ERR_SHAPE, "%s: sections hold %lld pairs, rot_dim=%d has %d", fn, pairs,
+                    rot_dim, rot_dim / 2);
+    if (n == 0 || T == 0)
+        return ok();
+    if (!rows || (rot_dim > 0 && (!pos || !inv_freq)))
+        return fail(TQ_ERR_NULL, "%s: a required pointer is NULL", fn);
+    if (n_axes > 1 && pos_stride < T)
+        return fail(TQ_ERR_SHAPE, "%s: pos_stride=%lld is less than T=%d", fn,
+                    (long long)pos_stride, T);
+    if (!aligned(pos, 4) || !aligned(inv_freq, 4))
+        return fail(TQ_ERR_ALIGN, "%s: pos and inv_freq must be 4-byte aligned", fn);
+    tq::RopeRows r[tq::kRopeMaxRows];
+    int count = 0;
+    long long heads = 0;
+    for (int i = 0; i < n; ++i) {
+        const tq_rope_rows &e = rows[i];
+        if (e.heads < 0 || e.heads > 65536)
+            return fail(TQ_ERR_SHAPE, "%s: entry %d: heads=%d", fn, i, e.heads);
+        if (e.heads == 0)
+            continue;
+        if ((e.x_bf16 != nullptr) == (e.x_f32 != nullptr) ||
+            (e.y_bf16 != nullptr) == (e.y_f32 != nullptr))
+            return fail(TQ_ERR_VALUE, "%s: entry %d: exactly one x and one y must be given", fn, i);
+        tq::RopeRows &o = r[count++];
+        o = tq::RopeRows{e.x_bf16, e.x_f32, e.y_bf16, e.y_f32, 0, 0, e.heads};
+        const long long packed = (long long)e.heads * head_dim;
+        tq_status st =
+            e.x_f32 ? check_rows(fn, "x", e.x_f32, e.x_stride, packed, 4, &o.x_stride)
+                    : check_rows(fn, "x", e.x_bf16, e.x_stride, packed, 2, &o.x_stride);
+        if (st == TQ_OK)
+            st = e.y_f32 ? check_rows(fn, "y", e.y_f32, e.y_stride, packed, 4, &o.y_stride)
+                         : check_rows(fn, "y", e.y_bf16, e.y_stride, packed, 2, &o.y_stride);
+        if (st != TQ_OK)
+            return st;
+        const void *x = e.x_f32 ? (const void *)e.x_f32 : e.x_bf16;
+        const void *y = e.y_f32 ? (const void *)e.y_f32 : e.y_bf16;
+        if (x == y && ((e.x_f32 != nullptr) != (e.y_f32 != nullptr) || o.x_stride != o.y_stride))
+            return fail(TQ_ERR_VALUE, "%s: entry %d: in place needs one type and one stride", fn, i);
+        heads += e.heads;
+    }
+    if (count == 0)
+        return ok();
+    // units of one CTA (four tokens at most) are counted in 32 bits
+    if (heads * (head_dim / 8) > (1ll << 28))
+        return fail(TQ_ERR_UNSUPPORTED, "%s: %lld heads of %d", fn, heads, head_dim);
+    cudaError_t e = tq::launch_rope(r, count, pos, pos_stride, inv_freq, sections, n_axes, T,
+                                    head_dim, rot_dim, (flags & TQ_ROPE_INTERLEAVED) != 0, stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+size_t tq_kv4_page_bytes(int page_size, int kv_heads, int head_dim)
+{
+    if ((page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) ||
+        (head_dim != 64 && head_dim != 128) || kv_heads < 1)
+        return 0;
+    return size_t(page_size) * size_t(kv_heads) * size_t(head_dim + 4);
+}
+
+tq_status tq_kv4_append(const tq_kv4_cache *cache, const uint16_t *k_bf16,
+                        const uint16_t *v_bf16, const float *k_f32, const float *v_f32,
+                        int64_t k_stride, int64_t v_stride, const int32_t *tok_start,
+                        const int32_t *lens, int T, cudaStream_t stream)
+{
+    const char *fn = "tq_kv4_append";
+    tq::Kv4View c;
+    tq_status st = check_kv4_cache(fn, cache, &c);
+    if (st != TQ_OK)
+        return st;
+    if (T < 0 || (!tok_start && T != cache->batch))
+        return fail(TQ_ERR_SHAPE, "%s: T=%d (without tok_start it is the batch, %d)", fn, T,
+                    cache->batch);
+    if (T == 0 || cache->batch == 0)
+        return ok();
+    const bool f32 = k_f32 || v_f32;
+    if (f32 ? (!k_f32 || !v_f32 || k_bf16 || v_bf16) : (!k_bf16 || !v_bf16))
+        return fail(TQ_ERR_VALUE, "%s: exactly one of the pairs k_bf16, v_bf16 and k_f32, v_f32 "
+                    "must be given", fn);
+    if (!lens)
+        return fail(TQ_ERR_NULL, "%s: lens is NULL", fn);
+    if (!aligned(lens, 4) || !aligned(tok_start, 4))
+        return fail(TQ_ERR_ALIGN, "%s: lens and tok_start must be 4-byte aligned", fn);
+    const void *k = f32 ? (const void *)k_f32 : k_bf16;
+    const void *v = f32 ? (const void *)v_f32 : v_bf16;
+    const long long packed = (long long)cache->kv_heads * cache->head_dim;
+    long long ks, vs;
+    if ((st = check_rows(fn, "k", k, k_stride, packed, f32 ? 4 : 2, &ks)) != TQ_OK ||
+        (st = check_rows(fn, "v", v, v_stride, packed, f32 ? 4 : 2, &vs)) != TQ_OK ||
+        (st = kv4_error_word(fn, &c)) != TQ_OK)
+        return st;
+    cudaError_t e = tq::launch_kv4_append(c, cache->head_dim, k, v, f32, ks, vs, tok_start, lens,
+                                          T, stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+tq_status tq_kv4_decode_workspace(const tq_kv4_cache *cache, int q_heads, size_t *bytes)
+{
+    const char *fn = "tq_kv4_decode_workspace";
+    tq::Kv4View c;
+    tq_status st = check_kv4_cache(fn, cache, &c);
+    if (st == TQ_OK)
+        st = check_kv4_heads(fn, cache, q_heads);
+    if (st != TQ_OK)
+        return st;
+    if (!bytes)
+        return fail(TQ_ERR_NULL, "%s: bytes is NULL", fn);
+    *bytes = 0;
+    return ok();
+}
+
+tq_status tq_kv4_prefill_workspace(const tq_kv4_cache *cache, int q_heads, int T, size_t *bytes)
+{
+    const char *fn = "tq_kv4_prefill_workspace";
+    tq::Kv4View c;
+    tq_status st = check_kv4_cache(fn, cache, &c);
+    if (st == TQ_OK)
+        st = check_kv4_heads(fn, cache, q_heads);
+    if (st != TQ_OK)
+        return st;
+    if (T < 0)
+        return fail(TQ_ERR_SHAPE, "%s: T=%d", fn, T);
+    if (!bytes)
+        return fail(TQ_ERR_NULL, "%s: bytes is NULL", fn);
+    *bytes = 0;
+    return ok();
+}
+
+tq_status tq_kv4_decode(const tq_kv4_cache *cache, const tq_kv4_query *query,
+                        const int32_t *lens, void *workspace, size_t workspace_bytes,
+                        cudaStream_t stream)
+{
+    const char *fn = "tq_kv4_decode";
+    tq::Kv4View c;
+    tq::Kv4Query q;
+    tq_status st = check_kv4_cache(fn, cache, &c);
+    if (st != TQ_OK)
+        return st;
+    if (cache->batch == 0)
+        return ok();
+    size_t need = 0;
+    if ((st = check_kv4_query(fn, cache, query, &q)) != TQ_OK ||
+        (st = tq_kv4_decode_workspace(cache, query->q_heads, &need)) != TQ_OK ||
+        (st = check_workspace(fn, workspace, workspace_bytes, need)) != TQ_OK)
+        return st;
+    if (!lens)
+        return fail(TQ_ERR_NULL, "%s: lens is NULL", fn);
+    if (!aligned(lens, 4))
+        return fail(TQ_ERR_ALIGN, "%s: lens must be 4-byte aligned", fn);
+    if ((st = kv4_error_word(fn, &c)) != TQ_OK)
+        return st;
+    cudaError_t e = tq::launch_kv4_attn(c, cache->head_dim, q, nullptr, lens, cache->batch, stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+tq_status tq_kv4_prefill(const tq_kv4_cache *cache, const tq_kv4_query *query,
+                         const int32_t *tok_start, const int32_t *lens, int T, void *workspace,
+                         size_t workspace_bytes, cudaStream_t stream)
+{
+    const char *fn = "tq_kv4_prefill";
+    tq::Kv4View c;
+    tq::Kv4Query q;
+    tq_status st = check_kv4_cache(fn, cache, &c);
+    if (st != TQ_OK)
+        return st;
+    if (T < 0)
+        return fail(TQ_ERR_SHAPE, "%s: T=%d", fn, T);
+    if (cache->batch == 0 || T == 0)
+        return ok();
+    size_t need = 0;
+    if ((st = check_kv4_query(fn, cache, query, &q)) != TQ_OK ||
+        (st = tq_kv4_prefill_workspace(cache, query->q_heads, T, &need)) != TQ_OK ||
+        (st = check_workspace(fn, workspace, workspace_bytes, need)) != TQ_OK)
+        return st;
+    if (!tok_start || !lens)
+        return fail(TQ_ERR_NULL, "%s: tok_start or lens is NULL", fn);
+    if (!aligned(lens, 4) || !aligned(tok_start, 4))
+        return fail(TQ_ERR_ALIGN, "%s: lens and tok_start must be 4-byte aligned", fn);
+    if ((st = kv4_error_word(fn, &c)) != TQ_OK)
+        return st;
+    cudaError_t e = tq::launch_kv4_attn(c, cache->head_dim, q, tok_start, lens, T, stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
 
 const char *tq_status_string(tq_status s)
 {

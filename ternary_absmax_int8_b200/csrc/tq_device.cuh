@@ -12,6 +12,7 @@ namespace tq {
 // (defined in tq_api.cu, read and cleared by tq_device_error()); its address
 // reaches them through their launch parameters.
 constexpr unsigned kErrWaitTimeout = 1u;  // a bounded pipeline wait gave up
+constexpr unsigned kErrBadPage = 2u;      // a page or length outside the cache was met
 
 // A pipeline wait that has not completed after this many nanoseconds of
 // global time gives up: it sets the error word and the kernel winds down.

@@ -283,6 +283,47 @@ struct BinMmaParams {
 // M == 1: the warp-MMA kernel; M = 2..4: the dp4a kernel.
 cudaError_t launch_binary_gemv(BinEntry *entries, int n, int M, cudaStream_t stream);
 
+// ------------------------------------------------------ rotary positions
+constexpr int kRopeMaxRows = 4;  // entries of a call
+constexpr int kRopeMaxAxes = 4;
+
+// One tensor of rows [T, heads, D]: exactly one input and one output type.
+struct RopeRows {
+    const uint16_t *x_bf16;
+    const float *x_f32;
+    uint16_t *y_bf16;
+    float *y_f32;
+    long long x_stride, y_stride;  // elements between tokens
+    int heads;
+};
+
+cudaError_t launch_rope(const RopeRows *rows, int n, const int32_t *pos, long long pos_stride,
+                        const float *inv_freq, const int *sections, int n_axes, int T, int D,
+                        int rot, bool interleaved, cudaStream_t stream);
+
+// ------------------------------------------- the 4-bit key/value cache
+struct Kv4View;  // kv4_common.cuh
+
+constexpr int kKv4MaxGroup = 64;  // query heads per key/value head
+
+// Queries [T, q_heads, D] (bf16), outputs bf16 [T, q_heads, D] and,
+// where not null, the logarithms of the softmax sums [T, q_heads].
+struct Kv4Query {
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;
+    long long q_stride, out_stride;  // elements between tokens
+    int q_heads;
+    int window;  // keys a query sees at most; 0: all before it
+    float scale;
+};
+
+cudaError_t launch_kv4_append(const Kv4View &c, int D, const void *k, const void *v, bool f32,
+                              long long k_stride, long long v_stride, const int32_t *tok_start,
+                              const int32_t *lens, int T, cudaStream_t stream);
+cudaError_t launch_kv4_attn(const Kv4View &c, int D, const Kv4Query &q, const int32_t *tok_start,
+                            const int32_t *lens, int T, cudaStream_t stream);
+
 // Device address of the library's error word on the current device.
 unsigned *device_error_word();
 
