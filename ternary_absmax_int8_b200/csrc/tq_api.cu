@@ -656,7 +656,7 @@ tq_status tq_kv4_decode_workspace(const tq_kv4_cache *cache, int q_heads, size_t
         return st;
     if (!bytes)
         return fail(TQ_ERR_NULL, "%s: bytes is NULL", fn);
-    *bytes = 0;
+    *bytes = tq::kv4_decode_workspace(c, cache->head_dim, q_heads);
     return ok();
 }
 
@@ -700,7 +700,7 @@ tq_status tq_kv4_decode(const tq_kv4_cache *cache, const tq_kv4_query *query,
         return fail(TQ_ERR_ALIGN, "%s: lens must be 4-byte aligned", fn);
     if ((st = kv4_error_word(fn, &c)) != TQ_OK)
         return st;
-    cudaError_t e = tq::launch_kv4_attn(c, cache->head_dim, q, nullptr, lens, cache->batch, stream);
+    cudaError_t e = tq::launch_kv4_decode(c, cache->head_dim, q, lens, workspace, stream);
     return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }
 

@@ -321,6 +321,9 @@ struct Kv4Query {
 cudaError_t launch_kv4_append(const Kv4View &c, int D, const void *k, const void *v, bool f32,
                               long long k_stride, long long v_stride, const int32_t *tok_start,
                               const int32_t *lens, int T, cudaStream_t stream);
+size_t kv4_decode_workspace(const Kv4View &c, int D, int q_heads);
+cudaError_t launch_kv4_decode(const Kv4View &c, int D, const Kv4Query &q, const int32_t *lens,
+                              void *workspace, cudaStream_t stream);
 cudaError_t launch_kv4_attn(const Kv4View &c, int D, const Kv4Query &q, const int32_t *tok_start,
                             const int32_t *lens, int T, cudaStream_t stream);
 

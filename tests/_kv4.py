@@ -6,10 +6,11 @@ Tolerance of attention outputs, per value. With p the softmax weights,
 A = sum_j p_j |v_j| and out = sum_j p_j v_j:
   - storing bf16 moves out by at most 2^-8 |out| (half a step);
   - a weight times its value's scale is rounded once to bf16 on its way into
-    the matrix units: 2^-8 of itself, in sum 2^-8 A (single tokens round to
-    fp16 against the largest value scale near it, 2^-11 of itself or 2^-25 of
-    that scale, which is less than 2^-8 A for the weights above 2^-15 that
-    carry the result);
+    the matrix units: 2^-8 of itself, in sum 2^-8 A. Single tokens round to
+    fp16 in units of 2^-14 of the largest value scale S near it: 2^-11 of
+    itself, or where that is smaller than fp16's last step of 2^-24, half of
+    it: 2^-25 2^-14 S = 2^-39 S. With codes up to 7, n keys move out by
+    7 n 2^-39 S = n 2^-39 max |v| (seen where one key takes all and its code is 0);
   - a query value may be held in fp16 against its row's largest: bf16's 8 bits
     fit, what falls below fp16's range moves by 2^-25 of the row's largest. The
     scores move by at most dz, so every weight by a factor within exp(+-2 dz)
@@ -139,7 +140,8 @@ def attention(cache, q, n, scale, window=0):
                         dq = 2.0 ** -25 * np.abs(x).max()
                         dz = scale * dq * np.abs(kk).sum(-1).max() + 2.0 ** -20 * size
                         tol[t, h] = (2.0 ** -8 * np.abs(out[t, h])
-                                     + A * (2.0 ** -8 + 2 * dz + 2.0 ** -12) + 1e-30)
+                                     + A * (2.0 ** -8 + 2 * dz + 2.0 ** -12)
+                                     + 2.0 ** -39 * len(vv) * np.abs(vv).max() + 1e-30)
                         ltol[t, h] = dz + 2.0 ** -18 + 2.0 ** -22 * abs(lse[t, h])
             t += 1
     return out, lse, tol, ltol
