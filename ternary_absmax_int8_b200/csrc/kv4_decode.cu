@@ -5,25 +5,31 @@
 // token and head. At 6.5 TB/s that is 13e12 codes a second against 36e12
 // instruction lanes, so a code may cost no more than about two lanes of work
 // from load to result, and scalar products cannot do it (4 query heads x 2
-// products). Hence the warp-level MMA (m16n8k16, fp16 x fp16 + fp32), with
-//  - keys on the 16-row side and the query heads that share them on the
-//    8-column side, S^T = K q^T and O^T = V^T P^T: 4 heads waste half of a
-//    product of 8 columns, not three quarters of one of 16 rows. (The
-//    tensor-memory MMA wants 64 or 128 rows and its operands in shared
-//    memory: codes would be written back there, 4 bytes for each one read.)
-//  - operands from the packed nibbles in nine instructions for eight codes: a
-//    nibble n masked in place under the exponent of 1024 (of 64, one nibble
-//    higher) is the fp16 number 1024 + n (64 + n), and one subtraction leaves
-//    the code, exactly. (Leaving out the subtraction, with masked nibbles as
-//    subnormals n 2^-24 and the +8 taken off the sums, costs five; but the
-//    matrix unit aligns a subnormal's products as if it were 2^-14, and the
-//    sums lost up to 2^-13 of the weights' sum.) Which 16 codes form an MMA's
-//    k range is free as long as both operands agree, so a lane takes
-//    contiguous bytes of a row and no data moves between lanes.
-//  - P^T from S^T's registers by one transposing move per 8 x 8 block.
-// Scores, running maxima and sums are fp32. A weight times its value's scale
-// is rounded to fp16 (2^-11) against the largest value scale of its tile, and
-// a tile's 64 products are added up by the MMA, the tiles in fp32 registers.
+// products). Hence the warp-level MMA, with keys on its 16-row side and the
+// query heads that share them on its 8-column side, S^T = K q^T and
+// O^T = V^T P^T. (The tensor-memory MMA wants 64 or 128 rows and its operands
+// in shared memory: codes would be written back there, 4 bytes for each one
+// read.) Which codes form an MMA's k range is free as long as both operands
+// agree, so a lane takes contiguous bytes of a row and nothing moves between
+// lanes but P, by one transposing move per 8 x 8 block.
+//  - Scores: m16n8k32, u8 x s8 -> s32. A word of 8 codes masked with 0F0F0F0F
+//    and F0F0F0F0 is two operand registers as it stands (the upper one 16
+//    times too large): two instructions for eight codes. The query is a whole
+//    number of 23 bits in three signed bytes, against the power of two above
+//    its head's largest value; they fill the columns that 4 heads would leave
+//    empty: upper and middle byte of head t in columns 2t and 2t + 1, the lower
+//    byte in a second product. The sums are exact; -8 sum(q), for the stored
+//    code + 8, is their starting value.
+//  - Values: m16n8k16 fp16. A nibble n masked in place under the exponent of
+//    1024 (of 64, one nibble higher) is the fp16 number 1024 + n (64 + n), and
+//    one subtraction leaves the code, exactly. (Leaving it out, with masked
+//    nibbles as subnormals n 2^-24 and the +8 taken off the sums, is cheaper
+//    by 4 in 10, but the matrix unit aligns a subnormal's products as if it
+//    were 2^-14: the results lost up to 2^-13 of the weights' sum.) Weights
+//    cannot be bytes: a long context holds many that are tiny and count.
+// Running maxima and sums are fp32. A weight times its value's scale is
+// rounded to fp16 (2^-11) against the largest value scale of its tile; a
+// tile's 64 products are added up by the MMA, the tiles in fp32 registers.
 //
 // Work split: the tiles (64 tokens of one sequence and head) of all sequences
 // form one list, cut into equal shares per SM and per warp, whatever the
@@ -45,33 +51,35 @@ namespace tq {
 
 namespace {
 
-constexpr int kTile = 64;  // tokens of a tile
+constexpr int kTile = 64;      // tokens of a tile
+constexpr int kMaxCtas = 160;  // of a launch: one per SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Warps of a CTA (one CTA per SM) and ring stages per warp: as many bytes in
-// flight as shared memory holds, with registers for the heads' results (NT
-// groups of 8 heads x D values x fp32 over 32 lanes).
-template <int D, int NT>
+// flight as shared memory holds, with registers for the heads' results. HG
+// groups of four heads share a pass over the codes.
+template <int D, int HG>
 struct DecodeShape {
-    static constexpr int kWarps = D == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 16 : 12);
-    static constexpr int kStages = D == 128 ? (NT == 1 ? 2 : 3) : (NT == 1 ? 3 : 4);
+    static constexpr int kWarps = HG == 4 ? 8 : D == 128 ? 12 : 16;
+    static constexpr int kStages = D == 128 ? (HG == 4 ? 3 : 2) : (HG == 4 ? 6 : 3);
     static constexpr int kStageBytes = kTile * (D + 4);
-    static constexpr int kHeads = 8 * NT;          // heads of an item
-    static constexpr int kPartFloats = D + 2;      // one head's part: values, maximum, sum
+    static constexpr int kHeads = 4 * HG;      // heads of an item
+    static constexpr int kPartFloats = D + 2;  // one head's part: values, maximum, sum
 };
+
+struct Crossing;
 
 struct DecodeParams {
     Kv4View c;
     Kv4Query q;
     const int32_t *lens;
     int rep;     // query heads per key/value head
-    int groups;  // of up to 8 NT query heads each
+    int groups;  // items per key/value head: of up to 4 HG query heads each
+    int rows;    // heads of a part: min(rep, 4 HG)
     // workspace
-    long long *total;  // tiles of the call
-    long long *start;  // [items] first tile of each item that has any
-    float *parts;      // [workers][2][rows][D + 2]
-    int rows;          // heads of a part: min(rep, 8 NT)
+    Crossing *crossing;  // [CTAs]
+    float *parts;               // [warps of all CTAs][2][rows][D + 2]
 };
 
 // A sequence's keys that its query sees: [begin, end), tiles of 64 from the
@@ -90,25 +98,27 @@ __device__ __forceinline__ Span span_of(const DecodeParams &p, int b)
     return s;
 }
 
-// Shares: CTA c of n takes tiles [c total / n, (c + 1) total / n), its warp w
-// of them [w per, (w + 1) per) with per = ceil(count / warps).
+// Shares: of n CTAs each takes total / n tiles, the first total % n one more;
+// warp w takes [w per, (w + 1) per) of them, per = ceil(count / warps).
 struct Share {
-    long long first;
-    int count, per;
+    int first, count, per;
 };
 
-__device__ __forceinline__ Share share_of(long long total, int cta, int ctas, int warps)
+__device__ __forceinline__ Share share_of(int total, int cta, int ctas, int warps)
 {
+    const int each = total / ctas, more = total - each * ctas;
     Share s;
-    s.first = total * cta / ctas;
-    s.count = int(total * (cta + 1) / ctas - s.first);
+    s.first = cta * each + min(cta, more);
+    s.count = each + (cta < more);
     s.per = (s.count + warps - 1) / warps;
     return s;
 }
 
-__device__ __forceinline__ int cta_of(long long tile, long long total, int ctas)
+__device__ __forceinline__ int cta_of(int tile, int total, int ctas)
 {
-    return int(((tile + 1) * ctas - 1) / total);
+    const int each = total / ctas, more = total - each * ctas;
+    const int split = more * (each + 1);  // tiles of the CTAs that take one more
+    return tile < split ? tile / (each + 1) : more + (tile - split) / each;
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -117,6 +127,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
                  "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, "
+                 "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
@@ -142,13 +161,21 @@ __device__ __forceinline__ uint32_t sub_half2(uint32_t v, uint32_t c)
                               *reinterpret_cast<const __half2 *>(&c));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
+// (w & mask) | c in one instruction: left to itself the compiler takes two,
+// as only one of the constants fits the instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t c)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(c));
+    return r;
+}
 __device__ __forceinline__ uint32_t low4(uint32_t w)
 {
-    return sub_half2((w & 0x000F000Fu) | 0x64006400u, 0x64086408u);  // 1024 + n - 1032
+    return sub_half2(and_or(w, 0x000F000Fu, 0x64006400u), 0x64086408u);  // 1024 + n - 1032
 }
 __device__ __forceinline__ uint32_t high4(uint32_t w)
 {
-    return sub_half2((w & 0x00F000F0u) | 0x54005400u, 0x54805480u);  // 64 + n - 72
+    return sub_half2(and_or(w, 0x00F000F0u, 0x54005400u), 0x54805480u);  // 64 + n - 72
 }
 
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi)
@@ -167,94 +194,153 @@ __device__ __forceinline__ int token_at(int i)
     return (i & 8) + ((j & 1) ? 4 + ((j >> 1) ^ 1) : j >> 1);
 }
 
-// One head group's running result over part of a sequence.
-template <int D, int NT>
+// The heads' running results over part of a sequence. Lane (g, t) holds head
+// 4j + t of group j: elements d and d + 1 of d-tile i at o[j / 2][i][j % 2] and
+// [2 + j % 2], d = g D/8 + 2 i.
+template <int D, int HG>
 struct Running {
-    float o[NT][D / 16][4];  // [d-tile]: elements d (0, 1) and d + 1 (2, 3) of heads 2t, 2t + 1
-    float m[NT][2], l[NT][2];
+    static constexpr int kV = (HG + 1) / 2;  // value products' column tiles
+    float o[kV][D / 16][4];
+    float m[HG], l[HG];  // maximum (accumulator x key scale), sum over the lane's tokens
 
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int v = 0; v < kV; ++v)
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    o[n][i][j] = 0.0f;
+                    o[v][i][j] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                l[n][j] = 0.0f;
-                m[n][j] = -INFINITY;
-            }
+        for (int j = 0; j < HG; ++j) {
+            m[j] = -INFINITY;
+            l[j] = 0.0f;
         }
     }
 };
 
-// A head group's queries as MMA operands, with what their scaling needs.
-template <int D, int NT>
+// The heads' queries as MMA operands: [column tile][high, low nibbles][k step].
+template <int D, int HG>
 struct Queries {
-    uint32_t b[NT][D / 16][2];
-    float mul[NT][2];  // accumulator x key scale -> log2 of the weight; heads 2t, 2t + 1
+    static constexpr int kT = HG + (HG + 1) / 2;  // upper + middle bytes, then lower bytes
+    uint32_t b[kT][2][D / 64][2];
+    int init[kT][2];  // -128 sum of the column's bytes; columns 2t, 2t + 1
+    float mul[HG];    // accumulator x key scale -> log2 of the weight; head 4j + t
 };
 
-template <int D, int NT>
-__device__ __forceinline__ void load_queries(const DecodeParams &p, long long row, int head0,
-                                             int heads, Queries<D, NT> &q)
+// Lane (g, t) takes part t of head 4j + g/2 of each group j: bf16 as stored.
+template <int D, int HG>
+__device__ __forceinline__ void fetch_queries(const DecodeParams &p, long long row, int head0,
+                                              int heads, uint4 (&raw)[HG][D / 32])
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        // lane's D/4 consecutive values of head 8n + g
-        float v[D / 4];
-        const bool real = n * 8 + g < heads;
+    for (int j = 0; j < HG; ++j) {
+        const int h = 4 * j + (g >> 1);
+        const bool real = h < heads;
         const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q.q + row + (long long)(head0 + (real ? n * 8 + g : 0)) * D + t * (D / 4));
+            p.q.q + row + (long long)(head0 + (real ? h : 0)) * D + t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            raw[j][i] = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+    }
+}
+
+// Its values go into both columns of a pair: upper byte in the even one,
+// middle in the odd.
+template <int D, int HG>
+__device__ __forceinline__ void convert_queries(const DecodeParams &p,
+                                                const uint4 (&raw)[HG][D / 32],
+                                                Queries<D, HG> &q)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint32_t y[HG][D / 4];  // the values' three bytes
+    float mul[HG];
+#pragma unroll
+    for (int j = 0; j < HG; ++j) {
+        float v[D / 4];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-            const uint4 u = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+            const uint4 u = raw[j][i];
             v[8 * i] = bf16_lo(u.x), v[8 * i + 1] = bf16_hi(u.x);
             v[8 * i + 2] = bf16_lo(u.y), v[8 * i + 3] = bf16_hi(u.y);
             v[8 * i + 4] = bf16_lo(u.z), v[8 * i + 5] = bf16_hi(u.z);
             v[8 * i + 6] = bf16_lo(u.w), v[8 * i + 7] = bf16_hi(u.w);
         }
-        // Scaled by a power of two so that the largest magnitude of the head
-        // lies in [2^14, 2^15): bf16's 8 bits fit fp16's 11.
+        // As multiples of 2^(k - 21), 2^k <= the head's largest magnitude
+        // < 2^(k + 1): bf16 values down to 2^-14 of it are exact.
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < D / 4; ++i)
             top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int k = min(max(int(top >> 23) - 127, -100), 117);
-        const float up = __uint_as_float(uint32_t(14 - k + 127) << 23);
+        const int k = max(int(top >> 23) - 127, -100);
+        const float up = __uint_as_float(uint32_t(21 - k + 127) << 23);
+        // Adding 1.5 2^23 leaves the whole number in the low bits; with 128
+        // added in each byte, a byte less 128 is the signed digit.
 #pragma unroll
-        for (int u = 0; u < D / 32; ++u)  // one 32-bit word of a key row: 8 codes
+        for (int i = 0; i < D / 4; ++i)
+            y[j][i] = __float_as_uint(fmaf(v[i], up, 12582912.0f)) - 0x4B400000u + 0x00808080u;
+        // the unit, scale and the change to base 2; an infinite or NaN query
+        // makes all of its head's scores NaN
+        mul[j] = __uint_as_float(uint32_t(k - 21 + 127) << 23) * (p.q.scale * kLog2e);
+        if (top >= 0x7F800000u)
+            mul[j] = NAN;
+        q.mul[j] = __shfl_sync(0xffffffffu, mul[j], 8 * t);
+    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                q.b[n][2 * u + (i >> 1)][i & 1] = pack_half(v[8 * u + i] * up, v[8 * u + 4 + i] * up);
-        // 1 / up, scale and the change to base 2
-        const float mul = __uint_as_float(uint32_t(k - 14 + 127) << 23) * (p.q.scale * kLog2e);
+    for (int c = 0; c < Queries<D, HG>::kT; ++c) {
+        // Lower bytes: of group 2 (c - HG) in the even column, of the next in
+        // the odd one.
+        const bool lower = c >= HG;
+        const int j0 = lower ? 2 * (c - HG) : c;
+        const bool odd = g & 1;
+        const uint32_t pick = lower ? 0u : odd ? 1u : 2u;  // byte of y
+        const uint32_t sel = pick | (pick + 4) << 4;       // of two values
+        int sum = 0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            q.mul[n][j] = __shfl_sync(0xffffffffu, mul, 8 * t + 4 * j);
+        for (int u = 0; u < D / 32; ++u)  // a word of a key row: 8 codes
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // its high nibbles: odd elements; its low
+                uint32_t z[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = 8 * u + 2 * i + (half == 0);
+                    z[i] = y[j0][e];
+                    if (lower)  // a group beyond the last: digits 0
+                        z[i] = odd ? (j0 + 1 < HG ? y[j0 + 1 < HG ? j0 + 1 : j0][e] : 0x80u) : z[i];
+                }
+                const uint32_t w = __byte_perm(__byte_perm(z[0], z[1], sel),
+                                               __byte_perm(z[2], z[3], sel), 0x5410) ^
+                                   0x80808080u;
+                sum = __dp4a(int(w), 0x01010101, sum);
+                q.b[c][half][u >> 1][u & 1] = w;
+            }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        q.init[c][0] = -128 * __shfl_sync(0xffffffffu, sum, 8 * t);
+        q.init[c][1] = -128 * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
     }
 }
 
 // One tile: scores, softmax step, weighted values. `sps` tokens of the tile
 // come from one page: in shared memory its key codes, value codes, key scales
-// and value scales follow one another, blocks of sps (D + 4) bytes. With
-// kEdge, tokens outside [begin, end) and pages whose bit of `good` is clear
-// take no part.
-template <int D, int NT, bool kEdge>
+// and value scales follow one another, blocks of sps (D + 4) bytes. Tokens
+// outside [begin, end) and pages whose bit of `good` is clear take no part
+// (tested in every tile: a second copy of this code without the tests costs a
+// short call more in instruction fetches than a long one gains).
+template <int D, int HG>
 __device__ __forceinline__ void tile_step(const uint8_t *stage, int lg_sps, int j0, int begin,
-                                          int end, uint32_t good, const Queries<D, NT> &q,
-                                          Running<D, NT> &r)
+                                          int end, uint32_t good, const Queries<D, HG> &q,
+                                          Running<D, HG> &r)
 {
+    constexpr int kV = Running<D, HG>::kV, kT = Queries<D, HG>::kT;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int sps = 1 << lg_sps;
     const int row0 = token_at(g);
-    float x[NT][4][4];
+    float x[HG][4][2];
     uint32_t sv[4][2];  // value scales (fp32 bits) of rows g and g + 8
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
@@ -281,36 +367,47 @@ __device__ __forceinline__ void tile_step(const uint8_t *stage, int lg_sps, int 
             w0[0] = a.x, w0[1] = a.y;
             w1[0] = b.x, w1[1] = b.y;
         }
+        int s[kT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[n][mt][i] = 0.0f;
-#pragma unroll
-        for (int u = 0; u < 2 * (D / 32); ++u) {
-            const uint32_t a = (u & 1) ? w0[u >> 1] >> 8 : w0[u >> 1];
-            const uint32_t b = (u & 1) ? w1[u >> 1] >> 8 : w1[u >> 1];
-            const uint32_t a0 = low4(a), a1 = low4(b), a2 = high4(a), a3 = high4(b);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                mma_f16(x[n][mt], a0, a1, a2, a3, q.b[n][u][0], q.b[n][u][1]);
+        for (int c = 0; c < kT; ++c) {
+            s[c][0] = s[c][2] = q.init[c][0];
+            s[c][1] = s[c][3] = q.init[c][1];
         }
-        bool in[2] = {true, true};
-        if constexpr (kEdge) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int j = j0 + mt * 16 + row0 + 8 * h;
-                in[h] = j >= begin && j < end && ((good >> blk) & 1u);
-                if (!in[h])
-                    sv[mt][h] = 0;
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t mask = half ? 0x0F0F0F0Fu : 0xF0F0F0F0u;
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u) {
+                const uint32_t a0 = w0[2 * u] & mask, a1 = w1[2 * u] & mask;
+                const uint32_t a2 = w0[2 * u + 1] & mask, a3 = w1[2 * u + 1] & mask;
+#pragma unroll
+                for (int c = 0; c < kT; ++c)
+                    mma_u8s8(s[c], a0, a1, a2, a3, q.b[c][half][u][0], q.b[c][half][u][1]);
+            }
+            if (half == 0) {  // the high nibbles stood for 16 times their codes
+#pragma unroll
+                for (int c = 0; c < kT; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[c][i] >>= 4;
             }
         }
+        bool in[2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int h = 0; h < 2; ++h) {
+            in[h] = unsigned(j0 + mt * 16 + row0 + 8 * h - begin) < unsigned(end - begin) &&
+                    ((good >> blk) & 1u);
+            if (!in[h])
+                sv[mt][h] = 0;
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float s = x[n][mt][i] * ks[i >> 1];
-                x[n][mt][i] = kEdge && !in[i >> 1] ? -INFINITY : s;
+        for (int j = 0; j < HG; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float upper = float(s[j][2 * h] * 256 + s[j][2 * h + 1]);
+                const float lower = float(s[HG + j / 2][2 * h + (j & 1)]);
+                const float z = fmaf(upper, 256.0f, lower) * ks[h];
+                x[j][mt][h] = in[h] ? z : -INFINITY;
             }
     }
 
@@ -325,74 +422,69 @@ __device__ __forceinline__ void tile_step(const uint8_t *stage, int lg_sps, int 
     const float sref = top == 0x7F800000u ? NAN : __uint_as_float(top - (14u << 23));
     const float rs = top == 0x7F800000u ? NAN : __uint_as_float((268u << 23) - top);
 
-    // Running maximum per head, in units of accumulator x key scale.
-    float mn[NT][2];
+    // Running maximum per head.
+    float mn[HG];
     bool grew = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int j = 0; j < HG; ++j) {
+        float v = fmaxf(x[j][0][0], x[j][0][1]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float v = fmaxf(x[n][0][j], x[n][0][2 + j]);
-#pragma unroll
-            for (int mt = 1; mt < 4; ++mt)
-                v = fmaxf(v, fmaxf(x[n][mt][j], x[n][mt][2 + j]));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            mn[n][j] = fmaxf(r.m[n][j], v);
-            grew = grew || mn[n][j] != r.m[n][j];
-        }
+        for (int mt = 1; mt < 4; ++mt)
+            v = fmaxf(v, fmaxf(x[j][mt][0], x[j][mt][1]));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        mn[j] = fmaxf(r.m[j], v);
+        grew = grew || mn[j] != r.m[j];
+    }
     if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float a[2];
+        for (int j = 0; j < HG; ++j) {
+            // nothing seen yet: nothing to scale (and no infinity minus itself)
+            const float a = r.m[j] == mn[j] ? 1.0f : ex2((r.m[j] - mn[j]) * q.mul[j]);
+            r.l[j] *= a;
+            r.m[j] = mn[j];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                // nothing seen yet: nothing to scale (and no infinity minus itself)
-                a[j] = r.m[n][j] == mn[n][j] ? 1.0f : ex2((r.m[n][j] - mn[n][j]) * q.mul[n][j]);
-                r.l[n][j] *= a[j];
-                r.m[n][j] = mn[n][j];
+            for (int i = 0; i < D / 16; ++i) {
+                r.o[j / 2][i][j & 1] *= a;
+                r.o[j / 2][i][2 + (j & 1)] *= a;
             }
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    r.o[n][i][j] *= a[j & 1];
         }
     }
 
     // Weights, and the operands P^T of the second product.
-    uint32_t pb[NT][4][2];
+    uint32_t pb[kV][4][2];
+    float c[HG];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float c[2];
+    for (int j = 0; j < HG; ++j)
+        c[j] = r.m[j] == -INFINITY ? 0.0f : -r.m[j] * q.mul[j];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            c[j] = r.m[n][j] == -INFINITY ? 0.0f : -r.m[n][j] * q.mul[n][j];
+    for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-            float w[4];
+        for (int h = 0; h < 2; ++h) {
+            const float by = __uint_as_float(sv[mt][h]) * rs;
+            float w[HG];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = ex2(fmaf(x[n][mt][i], q.mul[n][i & 1], c[i & 1]));
-                r.l[n][i & 1] += w[i];
-                w[i] *= __uint_as_float(sv[mt][i >> 1]) * rs;
+            for (int j = 0; j < HG; ++j) {
+                w[j] = ex2(fmaf(x[j][mt][h], q.mul[j], c[j]));
+                r.l[j] += w[j];
+                w[j] *= by;
             }
-            pb[n][mt][0] = transpose8x8(pack_half(w[0], w[1]));
-            pb[n][mt][1] = transpose8x8(pack_half(w[2], w[3]));
+#pragma unroll
+            for (int v = 0; v < kV; ++v)
+                pb[v][mt][h] = transpose8x8(pack_half(w[2 * v], 2 * v + 1 < HG ? w[2 * v + 1] : 0.0f));
         }
-    }
     // Values: lane g's D/8 consecutive elements, 8 (one word) at a time.
 #pragma unroll
     for (int u = 0; u < D / 64; ++u) {
-        float acc[NT][4][4];
+        float acc[kV][4][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int v = 0; v < kV; ++v)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    acc[n][i][j] = 0.0f;
+                    acc[v][i][j] = 0.0f;
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
             const int blk = (mt * 16) >> lg_sps;
@@ -415,62 +507,60 @@ __device__ __forceinline__ void tile_step(const uint8_t *stage, int lg_sps, int 
                 const uint32_t as = (i & 1) ? a >> 8 : a, bs = (i & 1) ? b >> 8 : b;
                 const uint32_t a0 = low4(as), a1 = high4(as), a2 = low4(bs), a3 = high4(bs);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    mma_f16(acc[n][i], a0, a1, a2, a3, pb[n][mt][0], pb[n][mt][1]);
+                for (int v = 0; v < kV; ++v)
+                    mma_f16(acc[v][i], a0, a1, a2, a3, pb[v][mt][0], pb[v][mt][1]);
             }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int j = 0; j < HG; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    r.o[n][4 * u + i][j] = fmaf(acc[n][i][j], sref, r.o[n][4 * u + i][j]);
+                for (int h = 0; h < 2; ++h) {
+                    float &o = r.o[j / 2][4 * u + i][2 * h + (j & 1)];
+                    o = fmaf(acc[j / 2][i][2 * h + (j & 1)], sref, o);
+                }
     }
 }
 
-// The lane's result for head 8n + 2t + j, element pair i: even, odd element.
-template <int D, int NT>
-__device__ __forceinline__ float2 value_pair(const Running<D, NT> &r, int n, int i, int j)
+// The lane's result for head 4j + t, element pair i.
+template <int D, int HG>
+__device__ __forceinline__ float2 value_pair(const Running<D, HG> &r, int j, int i)
 {
-    return make_float2(r.o[n][i][j], r.o[n][i][2 + j]);
+    return make_float2(r.o[j / 2][i][j & 1], r.o[j / 2][i][2 + (j & 1)]);
 }
 
 // The sums of weights lie spread over the lanes of a column: add them up.
-template <int D, int NT>
-__device__ __forceinline__ void close_sums(Running<D, NT> &r)
+template <int D, int HG>
+__device__ __forceinline__ void close_sums(Running<D, HG> &r)
 {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int j = 0; j < HG; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1)
-                r.l[n][j] += __shfl_xor_sync(0xffffffffu, r.l[n][j], o);
+        for (int o = 4; o <= 16; o <<= 1)
+            r.l[j] += __shfl_xor_sync(0xffffffffu, r.l[j], o);
 }
 
 // A part [heads][D + 2]: values, then the maximum (base 2) and the sum. For
 // heads beyond `rows` nothing is stored.
-template <int D, int NT>
-__device__ __forceinline__ void store_part(const Running<D, NT> &r, const Queries<D, NT> &q,
+template <int D, int HG>
+__device__ __forceinline__ void store_part(const Running<D, HG> &r, const Queries<D, HG> &q,
                                            float *part, int rows)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int j = 0; j < HG; ++j) {
+        const int h = 4 * j + t;
+        if (h >= rows)
+            continue;
+        float *row = part + h * (D + 2);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int h = 8 * n + 2 * t + j;
-            if (h >= rows)
-                continue;
-            float *row = part + h * (D + 2);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                *reinterpret_cast<float2 *>(row + g * (D / 8) + 2 * i) = value_pair(r, n, i, j);
-            if (g == 0)
-                *reinterpret_cast<float2 *>(row + D) = make_float2(
-                    r.m[n][j] == -INFINITY ? -INFINITY : r.m[n][j] * q.mul[n][j], r.l[n][j]);
-        }
+        for (int i = 0; i < D / 16; ++i)
+            *reinterpret_cast<float2 *>(row + g * (D / 8) + 2 * i) = value_pair(r, j, i);
+        if (g == 0)
+            *reinterpret_cast<float2 *>(row + D) =
+                make_float2(r.m[j] == -INFINITY ? -INFINITY : r.m[j] * q.mul[j], r.l[j]);
+    }
 }
 
 template <int D>
@@ -489,70 +579,89 @@ __device__ __forceinline__ float log_sum(float m, float l)
     return l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
-template <int D, int NT>
-__device__ __forceinline__ void store_final(const DecodeParams &p, const Running<D, NT> &r,
-                                            const Queries<D, NT> &q, int b, int head0, int heads)
+template <int D, int HG>
+__device__ __forceinline__ void store_final(const DecodeParams &p, const Running<D, HG> &r,
+                                            const Queries<D, HG> &q, int b, int head0, int heads)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int j = 0; j < HG; ++j) {
+        const int h = 4 * j + t;
+        if (h >= heads)
+            continue;
+        const float inv = inverse_sum(r.l[j]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int h = 8 * n + 2 * t + j;
-            if (h >= heads)
-                continue;
-            const float inv = inverse_sum(r.l[n][j]);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                store_out<D>(p, b, head0 + h, g * (D / 8) + 2 * i, value_pair(r, n, i, j), inv);
-            if (p.q.lse && g == 0)
-                p.q.lse[(long long)b * p.q.q_heads + head0 + h] =
-                    log_sum(r.m[n][j] * q.mul[n][j], r.l[n][j]);
-        }
-}
-
-// The weighted sum of one head's element pair d over n parts `stride` floats
-// apart, and that head's maximum and sum.
-template <int D, class PartAt>
-__device__ __forceinline__ void join(int n, PartAt part_at, int d, float2 *v, float *m, float *l)
-{
-    float top = -INFINITY;
-    for (int i = 0; i < n; ++i)
-        top = fmaxf(top, part_at(i)[D]);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float2 s = make_float2(0.0f, 0.0f);
-    float sum = 0.0f;
-    for (int i = 0; i < n; ++i) {
-        const float *part = part_at(i);
-        const float2 ml = *reinterpret_cast<const float2 *>(part + D);
-        const float2 x = *reinterpret_cast<const float2 *>(part + d);
-        const float w = ex2(ml.x - ref);
-        s.x = fmaf(w, x.x, s.x);
-        s.y = fmaf(w, x.y, s.y);
-        sum = fmaf(w, ml.y, sum);
+        for (int i = 0; i < D / 16; ++i)
+            store_out<D>(p, b, head0 + h, g * (D / 8) + 2 * i, value_pair(r, j, i), inv);
+        if (p.q.lse && g == 0)
+            p.q.lse[(long long)b * p.q.q_heads + head0 + h] = log_sum(r.m[j] * q.mul[j], r.l[j]);
     }
-    *v = s;
-    *m = top;
-    *l = sum;
 }
 
-struct Segment {  // a warp's last stretch, for the merge within the CTA
-    long long item;    // -1: none
-    long long first, last;  // the item's tiles [first, last) among all
+// Parts of one head joined one after another: v = sum_k 2^(m_k - m) v_k, and l
+// alike, m the largest m_k.
+struct Joined {
+    float2 v = make_float2(0.0f, 0.0f);
+    float m = -INFINITY, l = 0.0f;
+
+    __device__ __forceinline__ void rescale(float top)  // top >= m
+    {
+        const float a = m == top ? 1.0f : ex2(m - top);
+        v.x *= a;
+        v.y *= a;
+        l *= a;
+        m = top;
+    }
+    __device__ __forceinline__ void add_below(float2 x, float2 ml)  // ml.x <= m
+    {
+        const float b = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
+        v.x = fmaf(x.x, b, v.x);
+        v.y = fmaf(x.y, b, v.y);
+        l = fmaf(ml.y, b, l);
+    }
+    __device__ __forceinline__ void add(float2 x, float2 ml)
+    {
+        rescale(fmaxf(m, ml.x));
+        add_below(x, ml);
+    }
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(DecodeShape<D, NT>::kWarps * 32, 1)
+template <int D>
+__device__ __forceinline__ void store_joined(const DecodeParams &p, const Joined &r, int b,
+                                             int head, int d)
+{
+    store_out<D>(p, b, head, d, r.v, inverse_sum(r.l));
+    if (p.q.lse && d == 0)
+        p.q.lse[(long long)b * p.q.q_heads + head] = log_sum(r.m, r.l);
+}
+
+// The item that a CTA's share begins in, where it began in an earlier CTA: the
+// combine kernel's work list.
+struct Crossing {
+    int item;    // -1: none, or one that began further back than the CTA before
+    int parts;   // CTAs that hold a part of it, from the one before on
+    int warp0;   // the warp that it begins in there
+    int ended;   // its last part is in that CTA's first warp's slot 0
+};
+
+struct Segment {  // a warp's last stretch, for the merge within the CTA
+    int item;         // -1: none
+    int first, last;  // the item's tiles [first, last) among all
+};
+
+template <int D, int HG>
+__global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
     kv4_decode_kernel(const __grid_constant__ DecodeParams p)
 {
-    using S = DecodeShape<D, NT>;
+    using S = DecodeShape<D, HG>;
     constexpr int kThreads = S::kWarps * 32;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t bars[S::kWarps][S::kStages];
-    __shared__ long long scan[S::kWarps], s_total;
-    __shared__ long long warp_base[S::kWarps];  // tiles before the warp's first sequence
-    __shared__ int warp_b[S::kWarps];           // that sequence
+    __shared__ int scan[S::kWarps], scan2[S::kWarps];
+    __shared__ int warp_base[S::kWarps];  // tiles before the warp's first sequence
+    __shared__ int warp_b[S::kWarps];     // that sequence
     __shared__ Segment seg[S::kWarps];
+    __shared__ int ended[S::kWarps];  // item whose end is in the warp's slot 0, or -1
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0)
@@ -563,102 +672,138 @@ __global__ void __launch_bounds__(DecodeShape<D, NT>::kWarps * 32, 1)
     pdl_wait();
     pdl_launch_dependents();
 
-    // Tiles of all sequences.
+    // Tiles of all sequences; rows of a sequence without a visible token are
+    // written here, its CTA taken in turn. Up to 32 sequences each warp sums up
+    // for itself; beyond, the CTA does, a block of lengths at a time.
     const int hg = p.c.kv_heads * p.groups;
-    long long mine = 0;
-    for (int b = threadIdx.x; b < p.c.batch; b += kThreads)
-        mine += span_of(p, b).tiles;
-    for (int o = 16; o > 0; o >>= 1)
-        mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0)
-        scan[warp] = mine;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        long long sum = 0;
-        for (int w = 0; w < S::kWarps; ++w)
-            sum += scan[w];
-        s_total = sum * hg;
-        if (blockIdx.x == 0)
-            *p.total = sum * hg;
-    }
-    __syncthreads();
-    const long long total = s_total;
-    const Share share = share_of(total, blockIdx.x, gridDim.x, S::kWarps);
-    long long at = share.first + min(share.count, warp * share.per);
-    const long long stop = share.first + min(share.count, (warp + 1) * share.per);
-
-    // The sequence that holds each warp's first tile: a running sum over the
-    // lengths, a block of them at a time.
-    if (share.count > 0) {
-        long long before = 0;  // tiles (x hg) of the sequences before this block
-        for (int b0 = 0; b0 < p.c.batch && before <= share.first + share.count - 1; b0 += kThreads) {
-            const int b = b0 + threadIdx.x;
-            const long long n = b < p.c.batch ? (long long)span_of(p, b).tiles * hg : 0;
-            long long incl = n;
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o)
-                    incl += v;
+    auto tiles_of = [&](int b) {
+        if (b >= p.c.batch)
+            return 0;
+        return span_of(p, b).tiles * hg;
+    };
+    auto empty_rows = [&](int b, int n) {
+        if (n != 0 || b >= p.c.batch || b % int(gridDim.x) != int(blockIdx.x))
+            return;
+#pragma unroll 1
+        for (int h = 0; h < p.q.q_heads; ++h) {
+#pragma unroll 1
+            for (int d = 0; d < D; d += 2)
+                store_out<D>(p, b, h, d, make_float2(0.0f, 0.0f), 0.0f);
+            if (p.q.lse)
+                p.q.lse[(long long)b * p.q.q_heads + h] = -INFINITY;
+        }
+    };
+    auto running_sum = [&](int v) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o)
+                v += u;
+        }
+        return v;
+    };
+    Share share;
+    int at, stop, b = 0, seq0 = 0, total = 0;  // the warp's first sequence, tiles before it
+    if (p.c.batch <= 32) {
+        const int own = tiles_of(lane);
+        if (warp == S::kWarps - 1)
+            empty_rows(lane, own);
+        const int incl = running_sum(own);
+        total = __shfl_sync(0xffffffffu, incl, 31);
+        share = share_of(total, blockIdx.x, gridDim.x, S::kWarps);
+        at = share.first + min(share.count, warp * share.per);
+        stop = share.first + min(share.count, (warp + 1) * share.per);
+        b = min(31, __popc(__ballot_sync(0xffffffffu, incl <= at)));
+        seq0 = __shfl_sync(0xffffffffu, incl - own, b);
+    } else {
+        int mine = 0, own = 0;  // own: of the thread's sequence in the first block
+        for (int i = threadIdx.x; i < p.c.batch; i += kThreads) {
+            const int n = tiles_of(i);
+            mine += n;
+            if (i < kThreads)
+                own = n;
+            empty_rows(i, n);
+        }
+        int incl = running_sum(own);
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if (lane == 31) {
+            scan[warp] = incl;
+            scan2[warp] = mine;
+        }
+        __syncthreads();
+        int base = 0, before = 0;  // before: tiles of the sequences before this block
+        for (int w = 0; w < S::kWarps; ++w) {
+            total += scan2[w];
+            base += w < warp ? scan[w] : 0;
+            before += scan[w];
+        }
+        share = share_of(total, blockIdx.x, gridDim.x, S::kWarps);
+        at = share.first + min(share.count, warp * share.per);
+        stop = share.first + min(share.count, (warp + 1) * share.per);
+        auto place = [&](int i, int lo, int n) {  // sequence i has tiles [lo, lo + n)
+            for (int w = 0; w < S::kWarps; ++w) {
+                const int t = share.first + w * share.per;
+                if (w * share.per < share.count && t >= lo && t < lo + n) {
+                    warp_b[w] = i;
+                    warp_base[w] = lo;
+                }
             }
+        };
+        place(threadIdx.x, base + incl - own, own);
+        for (int b0 = kThreads; b0 < p.c.batch && before < share.first + share.count;
+             b0 += kThreads) {
+            own = tiles_of(b0 + threadIdx.x);
+            incl = running_sum(own);
             __syncthreads();
             if (lane == 31)
                 scan[warp] = incl;
             __syncthreads();
-            long long base = before, all = 0;
+            base = before;
             for (int w = 0; w < S::kWarps; ++w) {
-                if (w < warp)
-                    base += scan[w];
-                all += scan[w];
+                base += w < warp ? scan[w] : 0;
+                before += scan[w];
             }
-            const long long lo = base + incl - n;  // this sequence's tiles: [lo, lo + n)
-            for (int w = 0; w < S::kWarps; ++w) {
-                const long long t = share.first + (long long)w * share.per;
-                if (w * share.per < share.count && t >= lo && t < lo + n) {
-                    warp_b[w] = b;
-                    warp_base[w] = lo;
-                }
-            }
-            before += all;
+            place(b0 + threadIdx.x, base + incl - own, own);
+        }
+        __syncthreads();
+        if (at < stop) {
+            b = warp_b[warp];
+            seq0 = warp_base[warp];
         }
     }
-    __syncthreads();
 
     uint8_t *ring = smem + warp * (S::kStages * S::kStageBytes);
     const int worker = blockIdx.x * S::kWarps + warp;
     const int lg_sps = min(p.c.lg_ps, 6), sps = 1 << lg_sps;
     const int per_tile = kTile >> lg_sps;  // page stretches of a tile
     uint32_t phase = 0;                    // one bit per stage
-    Running<D, NT> run;
-    Queries<D, NT> qs;
+    Running<D, HG> run;
+    Queries<D, HG> qs;
     bool fine = true;
     Segment last{-1, 0, 0};
-    int b = 0;
-    long long seq0 = 0;
-    if (at < stop) {
-        b = warp_b[warp];
-        seq0 = warp_base[warp];
-    }
+    Crossing cross{-1, 0, 0, 0};
+    int end_item = -1;
     while (at < stop && fine) {
         Span sp = span_of(p, b);
-        while ((long long)sp.tiles * hg <= at - seq0 && b + 1 < p.c.batch) {
-            seq0 += (long long)sp.tiles * hg;  // on to the sequence with tile `at`
+        while (sp.tiles * hg <= at - seq0 && b + 1 < p.c.batch) {
+            seq0 += sp.tiles * hg;  // on to the sequence with tile `at`
             sp = span_of(p, ++b);
         }
-        if ((long long)sp.tiles * hg <= at - seq0)
+        if (sp.tiles * hg <= at - seq0)
             break;  // only if lengths change while the kernel runs
-        const int ig = int((at - seq0) / sp.tiles);  // head group of the sequence
-        const long long item0 = seq0 + (long long)ig * sp.tiles;
-        const int n0 = int(at - item0);
-        const int n1 = int(min((long long)sp.tiles, stop - item0));
+        const int ig = (at - seq0) / sp.tiles;  // head group of the sequence
+        const int item0 = seq0 + ig * sp.tiles;
+        const int n0 = at - item0;
+        const int n1 = min(sp.tiles, stop - item0);
         const int kvh = ig / p.groups, grp = ig - kvh * p.groups;
         const int head0 = kvh * p.rep + grp * S::kHeads;
         const int heads = min(S::kHeads, p.rep - grp * S::kHeads);
-        if (n0 == 0 && lane == 0)
-            p.start[(long long)b * hg + ig] = item0;
+        uint4 raw[HG][D / 32];
+        fetch_queries<D, HG>(p, b * p.q.q_stride, head0, heads, raw);
 
         // Page numbers of the next tiles, one lane each (a page of 128 tokens
         // serves two tiles); -1 for one outside the cache.
-        const int lg_batch = 5 - (6 - lg_sps);  // log2 of the tiles 32 lanes cover
+        const int lg_batch = lg_sps - 1;  // log2 of the tiles that 32 lanes cover
         int batch0 = -1, page = -1;
         const long long head_at = kvh * p.c.head_bytes<D>();
         auto fetch = [&](int n, int s) {  // tile n of the sequence into stage s
@@ -679,7 +824,7 @@ __global__ void __launch_bounds__(DecodeShape<D, NT>::kWarps * 32, 1)
             const int i0 = (n & ((1 << lg_batch) - 1)) * per_tile;
             uint8_t *dst = ring + s * S::kStageBytes;
             uint64_t *bar = &bars[warp][s];
-            const int pg = __shfl_sync(0xffffffffu, page, i0 + (per_tile > 1 ? lane % per_tile : 0));
+            const int pg = __shfl_sync(0xffffffffu, page, i0 + (lane & (per_tile - 1)));
             const uint32_t good = __ballot_sync(0xffffffffu, pg >= 0) & ((1u << per_tile) - 1u);
             if (lane == 0)
                 mbar_arrive_expect_tx(bar, __popc(good) * uint32_t(sps) * (D + 4));
@@ -704,7 +849,19 @@ __global__ void __launch_bounds__(DecodeShape<D, NT>::kWarps * 32, 1)
         uint32_t good = 0;  // four bits per stage: which stretches arrive
         for (int s = 0; s < S::kStages && n0 + s < n1; ++s)
             good |= fetch(n0 + s, s) << (4 * s);
-        load_queries<D, NT>(p, b * p.q.q_stride, head0, heads, qs);
+        if (n0 > 0 && at == share.first) {
+            // (while the first tile is on its way)
+            const Share s0 = share_of(total, blockIdx.x - 1, gridDim.x, S::kWarps);
+            if (item0 >= s0.first) {
+                const int end = item0 + sp.tiles, cta1 = cta_of(end - 1, total, gridDim.x);
+                const Share s1 = share_of(total, cta1, gridDim.x, S::kWarps);
+                cross.item = b * hg + ig;
+                cross.parts = cta1 - int(blockIdx.x) + 2;
+                cross.warp0 = (item0 - s0.first) / s0.per;
+                cross.ended = end < s1.first + min(s1.count, s1.per);
+            }
+        }
+        convert_queries<D, HG>(p, raw, qs);
         run.clear();
 #pragma unroll 1
         for (int n = n0, s = 0; n < n1; ++n, s = s + 1 == S::kStages ? 0 : s + 1) {
@@ -715,71 +872,85 @@ __global__ void __launch_bounds__(DecodeShape<D, NT>::kWarps * 32, 1)
             const uint8_t *stage = ring + s * S::kStageBytes;
             const int j0 = (sp.tile0 + n) * kTile;
             const uint32_t here = (good >> (4 * s)) & 15u;
-            if (j0 < sp.begin || j0 + kTile > sp.end || here != (1u << per_tile) - 1u)
-                tile_step<D, NT, true>(stage, lg_sps, j0, sp.begin, sp.end, here, qs, run);
-            else
-                tile_step<D, NT, false>(stage, lg_sps, j0, 0, 0, 0, qs, run);
+            tile_step<D, HG>(stage, lg_sps, j0, sp.begin, sp.end, here, qs, run);
             __syncwarp();
             if (n + S::kStages < n1)
                 good = (good & ~(15u << (4 * s))) | fetch(n + S::kStages, s) << (4 * s);
         }
         if (!fine)
             break;
-        close_sums<D, NT>(run);
+        close_sums<D, HG>(run);
         at = item0 + n1;
         if (n0 == 0 && n1 == sp.tiles) {
-            store_final<D, NT>(p, run, qs, b, head0, heads);
+            store_final<D, HG>(p, run, qs, b, head0, heads);
         } else if (n1 == sp.tiles && at < stop) {
             // the end of a sequence that other warps began
-            store_part<D, NT>(run, qs, p.parts + (long long)(2 * worker) * p.rows * (D + 2),
+            store_part<D, HG>(run, qs, p.parts + (long long)(2 * worker) * p.rows * (D + 2),
                               min(p.rows, heads));
+            end_item = b * hg + ig;
         } else {
-            last = Segment{(long long)b * hg + ig, item0, item0 + sp.tiles};
+            last = Segment{b * hg + ig, item0, item0 + sp.tiles};
         }
     }
 
-    // Merge the warps whose shares ended in one sequence.
-    if (lane == 0)
+    if (threadIdx.x == 0)
+        p.crossing[blockIdx.x] = cross;
+    // A part that no other warp of this CTA adds to needs no merge.
+    const bool alone = last.item >= 0 && fine &&
+                       (warp == 0 || last.first >= share.first + warp * share.per) &&
+                       (stop == share.first + share.count || last.last <= stop);
+    if (alone) {
+        store_part<D, HG>(run, qs, p.parts + (long long)(2 * worker + 1) * p.rows * (D + 2), p.rows);
+        last.item = -1;
+    }
+    // Merge what the CTA's warps hold of one sequence: the shares that ended in
+    // it (shared memory) and the one behind them that ended it and went on.
+    if (lane == 0) {
         seg[warp] = last;
-    __syncthreads();  // also: every ring is idle
+        ended[warp] = end_item;
+    }
+    if (!__syncthreads_or(last.item >= 0))  // also: every ring is idle
+        return;
+    float *mine_at = reinterpret_cast<float *>(smem) + warp * (S::kHeads * S::kPartFloats);
     if (last.item >= 0 && fine)
-        store_part<D, NT>(run, qs,
-                          reinterpret_cast<float *>(smem) + warp * (S::kHeads * S::kPartFloats),
-                          S::kHeads);
+        store_part<D, HG>(run, qs, mine_at, S::kHeads);
     __syncthreads();
-    for (int w = 0; w < S::kWarps;) {
+#pragma unroll 1
+    for (int w = 0; w < S::kWarps && w * share.per < share.count;) {
         const Segment s = seg[w];
         int n = 1;
         while (w + n < S::kWarps && s.item >= 0 && seg[w + n].item == s.item)
             ++n;
         if (s.item >= 0) {
-            const int sb = int(s.item / hg), ig = int(s.item - (long long)sb * hg);
+            const int sb = s.item / hg, ig = s.item - sb * hg;
             const int kvh = ig / p.groups, grp = ig - kvh * p.groups;
             const int head0 = kvh * p.rep + grp * S::kHeads;
             const int heads = min(S::kHeads, p.rep - grp * S::kHeads);
-            // complete if these warps hold all of it (a share that goes on
-            // past it would have been the end of a sequence, above)
-            const long long from = share.first + (long long)w * share.per;
-            const long long to = share.first + min(share.count, (w + n) * share.per);
-            const bool whole = from <= s.first && to >= s.last;
-            const float *first = reinterpret_cast<const float *>(smem) +
-                                 w * (S::kHeads * S::kPartFloats);
-            float *dst = p.parts +
-                         (long long)(2 * (blockIdx.x * S::kWarps + w) + 1) * p.rows * (D + 2);
+            const bool more = w + n < S::kWarps && ended[w + n] == s.item;
+            const int from = share.first + w * share.per;
+            const int to = share.first + min(share.count, (w + n) * share.per);
+            const bool whole = from <= s.first && (more || to >= s.last);
+            const float *first =
+                reinterpret_cast<const float *>(smem) + w * (S::kHeads * S::kPartFloats);
+            float *dst = p.parts + (long long)(2 * (blockIdx.x * S::kWarps + w) + 1) * p.rows * (D + 2);
+            const float *tail =
+                p.parts + (long long)(2 * (blockIdx.x * S::kWarps + w + n)) * p.rows * (D + 2);
             for (int i = threadIdx.x; i < heads * (D / 2); i += kThreads) {
                 const int h = i / (D / 2), d = 2 * (i - h * (D / 2));
-                float2 v;
-                float m, l;
-                join<D>(n, [&](int k) { return first + (k * S::kHeads + h) * S::kPartFloats; }, d,
-                        &v, &m, &l);
+                Joined r;
+#pragma unroll 1
+                for (int k = 0; k < n + more; ++k) {
+                    const float *x = k < n ? first + (k * S::kHeads + h) * S::kPartFloats
+                                           : tail + h * (D + 2);
+                    r.add(*reinterpret_cast<const float2 *>(x + d),
+                          *reinterpret_cast<const float2 *>(x + D));
+                }
                 if (whole) {
-                    store_out<D>(p, sb, head0 + h, d, v, inverse_sum(l));
-                    if (p.q.lse && d == 0)
-                        p.q.lse[(long long)sb * p.q.q_heads + head0 + h] = log_sum(m, l);
+                    store_joined<D>(p, r, sb, head0 + h, d);
                 } else {
-                    *reinterpret_cast<float2 *>(dst + h * (D + 2) + d) = v;
+                    *reinterpret_cast<float2 *>(dst + h * (D + 2) + d) = r.v;
                     if (d == 0)
-                        *reinterpret_cast<float2 *>(dst + h * (D + 2) + D) = make_float2(m, l);
+                        *reinterpret_cast<float2 *>(dst + h * (D + 2) + D) = make_float2(r.m, r.l);
                 }
             }
         }
@@ -787,111 +958,104 @@ __global__ void __launch_bounds__(DecodeShape<D, NT>::kWarps * 32, 1)
     }
 }
 
-// Joins the parts of each item that several CTAs (or a CTA's merged warps and
-// the warp behind them) hold, in the order of the tiles, and writes the rows
-// of sequences without a visible token. One CTA per item.
-template <int D, int NT>
-__global__ void __launch_bounds__(256) kv4_combine_kernel(const __grid_constant__ DecodeParams p,
-                                                          int ctas)
+// Joins the parts of each item that several CTAs hold, in the order of the
+// tiles. Block (c - 1, h): head h of the item that CTA c's share begins in, if
+// it began in CTA c - 1. Groups of D/2 threads take every kGroups-th part each,
+// so that all loads of a part list up to 32 long are in flight at once.
+constexpr int kCombineThreads = 256;
+
+template <int D, int HG>
+__global__ void __launch_bounds__(kCombineThreads)
+    kv4_combine_kernel(const __grid_constant__ DecodeParams p)
 {
-    using S = DecodeShape<D, NT>;
+    using S = DecodeShape<D, HG>;
+    constexpr int kGroups = kCombineThreads / (D / 2), kBatch = 8;
+    __shared__ float2 vs[kGroups][D / 2], mls[kGroups];
     pdl_wait();
     pdl_launch_dependents();
+    const int c0 = blockIdx.x, h = blockIdx.y;
+    const Crossing x = p.crossing[c0 + 1];
     const int hg = p.c.kv_heads * p.groups;
-    const int b = blockIdx.x / hg, ig = blockIdx.x - b * hg;
+    const int b = x.item / hg, ig = x.item - b * hg;
     const int kvh = ig / p.groups, grp = ig - kvh * p.groups;
-    const int head0 = kvh * p.rep + grp * S::kHeads;
-    const int heads = min(S::kHeads, p.rep - grp * S::kHeads);
-    const Span sp = span_of(p, b);
-    long long first = 0, end = 0, total = 1;
-    int cta0 = 0, cta1 = -1;
-    if (sp.tiles > 0) {
-        total = *p.total;
-        first = p.start[blockIdx.x];
-        end = first + sp.tiles;
-        cta0 = cta_of(first, total, ctas);
-        cta1 = cta_of(end - 1, total, ctas);
-        if (cta0 == cta1) {
-            // one CTA: whole there unless the warp behind the merged ones ended it
-            const Share s = share_of(total, cta0, ctas, S::kWarps);
-            const int w0 = int(first - s.first) / s.per, w1 = int(end - 1 - s.first) / s.per;
-            const long long stop1 = s.first + min(s.count, (w1 + 1) * s.per);
-            if (w0 == w1 || stop1 == end)
-                return;
+    if (x.item < 0 || h >= min(S::kHeads, p.rep - grp * S::kHeads))
+        return;
+    // A CTA holds its part in the slot 1 of the first of its warps that worked
+    // on it, or, where its first warp ended the item and went on, in slot 0.
+    const int n = x.parts;
+    const int group = threadIdx.x / (D / 2), d = 2 * (threadIdx.x % (D / 2));
+    Joined r;
+#pragma unroll 1
+    for (int k0 = group; k0 < n; k0 += kGroups * kBatch) {
+        float2 v[kBatch], ml[kBatch];
+        float top = r.m;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int k = k0 + i * kGroups;
+            v[i] = make_float2(0.0f, 0.0f);
+            ml[i] = make_float2(-INFINITY, 0.0f);
+            if (k < n) {
+                const int slot = 2 * ((c0 + k) * S::kWarps + (k == 0 ? x.warp0 : 0)) + 1 -
+                                 (k == n - 1 && x.ended);
+                const float *part = p.parts + ((long long)slot * p.rows + h) * (D + 2);
+                v[i] = *reinterpret_cast<const float2 *>(part + d);
+                ml[i] = *reinterpret_cast<const float2 *>(part + D);
+            }
         }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            top = fmaxf(top, ml[i].x);
+        r.rescale(top);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            r.add_below(v[i], ml[i]);
     }
-    // Part k of the item: per CTA the merged warps' part, then, in the last
-    // CTA, that of a warp that ended the item and went on.
-    __shared__ int slot[2 * 160];
-    __shared__ int slots;
-    if (threadIdx.x == 0) {
-        int n = 0;
-        for (int c = cta0; c <= cta1; ++c) {
-            const Share s = share_of(total, c, ctas, S::kWarps);
-            if (s.count == 0)
-                continue;
-            const int w0 = max(0, int(max(first, s.first) - s.first) / s.per);
-            const long long lim = min(end, s.first + s.count);
-            const int w1 = int(lim - 1 - s.first) / s.per;
-            const long long stop1 = s.first + min(s.count, (w1 + 1) * s.per);
-            const bool ended = lim == end && stop1 > end;  // w1 went on to the next item
-            if (w0 < w1 || !ended)
-                slot[n++] = 2 * (c * S::kWarps + w0) + 1;
-            if (ended)
-                slot[n++] = 2 * (c * S::kWarps + w1);
-        }
-        slots = n;
-    }
+    vs[group][d / 2] = r.v;
+    if (d == 0)
+        mls[group] = make_float2(r.m, r.l);
     __syncthreads();
-    const int n = slots;
-    for (int i = threadIdx.x; i < heads * (D / 2); i += blockDim.x) {
-        const int h = i / (D / 2), d = 2 * (i - h * (D / 2));
-        float2 v;
-        float m, l;
-        join<D>(n, [&](int k) {
-            return p.parts + ((long long)slot[k] * p.rows + h) * (D + 2);
-        }, d, &v, &m, &l);
-        store_out<D>(p, b, head0 + h, d, v, inverse_sum(l));
-        if (p.q.lse && d == 0)
-            p.q.lse[(long long)b * p.q.q_heads + head0 + h] = log_sum(m, l);
+    if (group == 0) {
+        for (int i = 1; i < kGroups; ++i)
+            r.add(vs[i][d / 2], mls[i]);
+        store_joined<D>(p, r, b, kvh * p.rep + grp * S::kHeads + h, d);
     }
 }
 
 struct DecodePlan {
-    int rep, nt, groups, rows, ctas, warps;
-    long long items;
-    size_t start_at, parts_at, bytes;
+    int rep, hg, groups, rows, ctas, warps;
+    long long items, tiles;  // tiles: at most so many
+    size_t parts_at, bytes;
 };
 
 DecodePlan plan_decode(const Kv4View &c, int D, int q_heads)
 {
     DecodePlan d;
     d.rep = q_heads / c.kv_heads;
-    d.nt = d.rep <= 8 ? 1 : 2;
-    d.groups = (d.rep + 8 * d.nt - 1) / (8 * d.nt);
-    d.rows = std::min(d.rep, 8 * d.nt);
-    d.ctas = std::min(device_sm_count(), 160);
-    d.warps = D == 128 ? (d.nt == 1 ? DecodeShape<128, 1>::kWarps : DecodeShape<128, 2>::kWarps)
-                       : (d.nt == 1 ? DecodeShape<64, 1>::kWarps : DecodeShape<64, 2>::kWarps);
+    d.hg = d.rep <= 4 ? 1 : d.rep <= 8 ? 2 : 4;
+    d.groups = (d.rep + 4 * d.hg - 1) / (4 * d.hg);
+    d.rows = std::min(d.rep, 4 * d.hg);
+    d.ctas = std::min(device_sm_count(), kMaxCtas);
+    d.warps = d.hg == 4 ? DecodeShape<128, 4>::kWarps
+                        : D == 128 ? DecodeShape<128, 1>::kWarps : DecodeShape<64, 1>::kWarps;
     d.items = (long long)c.batch * c.kv_heads * d.groups;
-    d.start_at = 16;
-    d.parts_at = (d.start_at + size_t(d.items) * sizeof(long long) + 15) & ~size_t(15);
+    d.tiles = d.items * ((c.max_len() + kTile - 1) / kTile);
+    d.parts_at = size_t(d.ctas) * sizeof(Crossing);
     d.bytes = d.parts_at +
               size_t(d.ctas) * d.warps * 2 * d.rows * size_t(D + 2) * sizeof(float);
     return d;
 }
 
-template <int D, int NT>
+template <int D, int HG>
 cudaError_t launch(const DecodeParams &p, const DecodePlan &plan, cudaStream_t stream)
 {
-    using S = DecodeShape<D, NT>;
+    using S = DecodeShape<D, HG>;
     constexpr size_t kSmem = size_t(S::kWarps) * S::kStages * S::kStageBytes;
     static_assert(size_t(S::kWarps) * S::kHeads * S::kPartFloats * 4 <= kSmem, "merge space");
     static thread_local int configured_dev = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && configured_dev != dev) {
-        e = cudaFuncSetAttribute(kv4_decode_kernel<D, NT>,
+        e = cudaFuncSetAttribute(kv4_decode_kernel<D, HG>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
         if (e == cudaSuccess)
             configured_dev = dev;
@@ -908,13 +1072,13 @@ cudaError_t launch(const DecodeParams &p, const DecodePlan &plan, cudaStream_t s
     cfg.gridDim = dim3(unsigned(plan.ctas));
     cfg.blockDim = dim3(S::kWarps * 32);
     cfg.dynamicSmemBytes = kSmem;
-    e = cudaLaunchKernelEx(&cfg, kv4_decode_kernel<D, NT>, p);
-    if (e != cudaSuccess)
-        return e;
-    cfg.gridDim = dim3(unsigned(plan.items));
-    cfg.blockDim = dim3(256);
+    e = cudaLaunchKernelEx(&cfg, kv4_decode_kernel<D, HG>, p);
+    if (e != cudaSuccess || plan.tiles == plan.items || plan.ctas == 1)
+        return e;  // at most one tile per item, or one CTA: nothing is shared
+    cfg.gridDim = dim3(unsigned(plan.ctas - 1), unsigned(plan.rows));
+    cfg.blockDim = dim3(kCombineThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D, NT>, p, plan.ctas);
+    return cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D, HG>, p);
 }
 
 }  // namespace
@@ -928,8 +1092,8 @@ cudaError_t launch_kv4_decode(const Kv4View &c, int D, const Kv4Query &q, const 
                               void *workspace, cudaStream_t stream)
 {
     const DecodePlan plan = plan_decode(c, D, q.q_heads);
-    if (plan.items > INT32_MAX)
-        return cudaErrorInvalidValue;
+    if (plan.items > INT32_MAX || plan.tiles > INT32_MAX - kTile)
+        return cudaErrorInvalidValue;  // tiles are counted in 32 bits
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     DecodeParams p;
     p.c = c;
@@ -937,13 +1101,16 @@ cudaError_t launch_kv4_decode(const Kv4View &c, int D, const Kv4Query &q, const 
     p.lens = lens;
     p.rep = plan.rep;
     p.groups = plan.groups;
-    p.total = reinterpret_cast<long long *>(ws);
-    p.start = reinterpret_cast<long long *>(ws + plan.start_at);
+    p.crossing = reinterpret_cast<Crossing *>(ws);
     p.parts = reinterpret_cast<float *>(ws + plan.parts_at);
     p.rows = plan.rows;
     if (D == 128)
-        return plan.nt == 1 ? launch<128, 1>(p, plan, stream) : launch<128, 2>(p, plan, stream);
-    return plan.nt == 1 ? launch<64, 1>(p, plan, stream) : launch<64, 2>(p, plan, stream);
+        return plan.hg == 1   ? launch<128, 1>(p, plan, stream)
+               : plan.hg == 2 ? launch<128, 2>(p, plan, stream)
+                              : launch<128, 4>(p, plan, stream);
+    return plan.hg == 1   ? launch<64, 1>(p, plan, stream)
+           : plan.hg == 2 ? launch<64, 2>(p, plan, stream)
+                          : launch<64, 4>(p, plan, stream);
 }
 
 }  // namespace tq
