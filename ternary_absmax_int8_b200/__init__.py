@@ -204,6 +204,9 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():
+            # the current stream's handle, without building a Stream object around it
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
         if not torch.cuda.is_available():
             return None
         return torch.cuda.current_stream().cuda_stream
@@ -361,15 +364,22 @@ def tq_device_error(reset: bool = False) -> int:
     return int(code.value)
 
 
-def _gpu_ptr(t, size: int):
-    """Pointer of a device tensor of `size`-byte elements on the current device (an int or
-    None passes through); a tensor elsewhere is refused, as the kernel would run here."""
+def _device() -> int:
+    """The current CUDA device, or -2 (no tensor's) where there is none."""
+    import torch
+    if torch.cuda.is_initialized() or torch.cuda.is_available():
+        return torch.cuda.current_device()
+    return -2
+
+
+def _gpu_ptr(t, size: int, device: int):
+    """Pointer of a tensor of `size`-byte elements on CUDA device `device`, the current one (an
+    int or None passes through); a tensor elsewhere is refused, as the kernel would run here."""
     if t is None or isinstance(t, int):
         return t
-    import torch
     if t.element_size() != size:
         raise TQError(4, f"a tensor of {size}-byte elements is wanted, not {t.dtype}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != device:
         raise TQError(4, f"a tensor on {t.device}: tensors must be on the current CUDA device")
     return t.data_ptr()
 
@@ -378,9 +388,10 @@ def make_rope_rows(rows, head_dim: int):
     """A table of ``tq_rope_rows`` from dicts with the keys x_bf16 or x_f32, y_bf16 or y_f32,
     heads and, for rows that are not packed, x_stride and y_stride (values between tokens)."""
     arr = (TqRopeRows * len(rows))()
+    dev = _device()
     for e, r in zip(arr, rows):
-        e.x_bf16, e.x_f32 = _gpu_ptr(r.get("x_bf16"), 2), _gpu_ptr(r.get("x_f32"), 4)
-        e.y_bf16, e.y_f32 = _gpu_ptr(r.get("y_bf16"), 2), _gpu_ptr(r.get("y_f32"), 4)
+        e.x_bf16, e.x_f32 = _gpu_ptr(r.get("x_bf16"), 2, dev), _gpu_ptr(r.get("x_f32"), 4, dev)
+        e.y_bf16, e.y_f32 = _gpu_ptr(r.get("y_bf16"), 2, dev), _gpu_ptr(r.get("y_f32"), 4, dev)
         e.heads = int(r["heads"])
         e.x_stride = int(r.get("x_stride", 0)) or e.heads * int(head_dim)
         e.y_stride = int(r.get("y_stride", 0)) or e.heads * int(head_dim)
@@ -390,9 +401,10 @@ def make_rope_rows(rows, head_dim: int):
 def tq_rope(rows, pos, inv_freq, sections, T: int, head_dim: int, rot_dim: int, flags: int = 0,
             pos_stride: int = 0, stream=None) -> None:
     """Rotary positions of the rows in a make_rope_rows table; pos int32 [len(sections), T]."""
+    dev = _device()
     n = len(sections)
-    _check(_load().tq_rope(rows, len(rows), _gpu_ptr(pos, 4), int(pos_stride) or int(T),
-                           _gpu_ptr(inv_freq, 4), (_i * n)(*sections), n, int(T), int(head_dim),
+    _check(_load().tq_rope(rows, len(rows), _gpu_ptr(pos, 4, dev), int(pos_stride) or int(T),
+                           _gpu_ptr(inv_freq, 4, dev), (_i * n)(*sections), n, int(T), int(head_dim),
                            int(rot_dim), int(flags), _stream(stream)))
 
 
@@ -404,7 +416,8 @@ def make_kv4_cache(pages=None, page_table=None, num_pages: int = 0, page_size: i
                    kv_heads: int = 1, head_dim: int = 128, batch: int = 0, max_pages: int = 0,
                    page_stride: int = 0) -> TqKv4Cache:
     """Describe a 4-bit key/value cache. It holds pointers only: keep the tensors."""
-    return TqKv4Cache(_gpu_ptr(pages, 1), _gpu_ptr(page_table, 4), int(page_stride),
+    dev = _device()
+    return TqKv4Cache(_gpu_ptr(pages, 1, dev), _gpu_ptr(page_table, 4, dev), int(page_stride),
                       int(num_pages), int(page_size), int(kv_heads), int(head_dim), int(batch),
                       int(max_pages))
 
@@ -412,9 +425,10 @@ def make_kv4_cache(pages=None, page_table=None, num_pages: int = 0, page_size: i
 def tq_kv4_append(cache, k_bf16, v_bf16, k_f32, v_f32, tok_start, lens, T: int, k_stride: int = 0,
                   v_stride: int = 0, stream=None) -> None:
     """Quantise new keys and values into the cache's pages (one of the two pairs)."""
-    _check(_load().tq_kv4_append(ctypes.byref(cache), _gpu_ptr(k_bf16, 2), _gpu_ptr(v_bf16, 2),
-                                 _gpu_ptr(k_f32, 4), _gpu_ptr(v_f32, 4), int(k_stride),
-                                 int(v_stride), _gpu_ptr(tok_start, 4), _gpu_ptr(lens, 4), int(T),
+    dev = _device()
+    _check(_load().tq_kv4_append(ctypes.byref(cache), _gpu_ptr(k_bf16, 2, dev), _gpu_ptr(v_bf16, 2, dev),
+                                 _gpu_ptr(k_f32, 4, dev), _gpu_ptr(v_f32, 4, dev), int(k_stride),
+                                 int(v_stride), _gpu_ptr(tok_start, 4, dev), _gpu_ptr(lens, 4, dev), int(T),
                                  _stream(stream)))
 
 
@@ -431,8 +445,8 @@ def tq_kv4_prefill_workspace(cache, q_heads: int, T: int) -> int:
     return size.value
 
 
-def _kv4_query(q, out, lse, q_heads, scale, window, q_stride, out_stride):
-    return ctypes.byref(TqKv4Query(_gpu_ptr(q, 2), _gpu_ptr(out, 2), _gpu_ptr(lse, 4),
+def _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride):
+    return ctypes.byref(TqKv4Query(_gpu_ptr(q, 2, dev), _gpu_ptr(out, 2, dev), _gpu_ptr(lse, 4, dev),
                                    int(q_stride), int(out_stride), int(q_heads),
                                    int(window), float(scale), 0))
 
@@ -441,16 +455,18 @@ def tq_kv4_decode(cache, q, lens, out, lse, q_heads: int, scale: float, window: 
                   workspace=None, workspace_bytes: int = 0, q_stride: int = 0,
                   out_stride: int = 0, stream=None) -> None:
     """Attention of one new token per sequence over the cache."""
-    query = _kv4_query(q, out, lse, q_heads, scale, window, q_stride, out_stride)
-    _check(_load().tq_kv4_decode(ctypes.byref(cache), query, _gpu_ptr(lens, 4),
-                                 _gpu_ptr(workspace, 1), int(workspace_bytes), _stream(stream)))
+    dev = _device()
+    query = _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride)
+    _check(_load().tq_kv4_decode(ctypes.byref(cache), query, _gpu_ptr(lens, 4, dev),
+                                 _gpu_ptr(workspace, 1, dev), int(workspace_bytes), _stream(stream)))
 
 
 def tq_kv4_prefill(cache, q, tok_start, lens, out, lse, T: int, q_heads: int, scale: float,
                    window: int = 0, workspace=None, workspace_bytes: int = 0, q_stride: int = 0,
                    out_stride: int = 0, stream=None) -> None:
     """Attention of any number of new tokens per sequence over the cache."""
-    query = _kv4_query(q, out, lse, q_heads, scale, window, q_stride, out_stride)
-    _check(_load().tq_kv4_prefill(ctypes.byref(cache), query, _gpu_ptr(tok_start, 4),
-                                  _gpu_ptr(lens, 4), int(T), _gpu_ptr(workspace, 1),
+    dev = _device()
+    query = _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride)
+    _check(_load().tq_kv4_prefill(ctypes.byref(cache), query, _gpu_ptr(tok_start, 4, dev),
+                                  _gpu_ptr(lens, 4, dev), int(T), _gpu_ptr(workspace, 1, dev),
                                   int(workspace_bytes), _stream(stream)))

@@ -1,0 +1,953 @@
+// kv4_prefill.cu -- attention of any number of new tokens per sequence over
+// the 4-bit cache (include/tq.h, tq_kv4_prefill), on the tensor cores.
+//
+// A CTA takes 256 query rows of one sequence and key/value head, a row being
+// (token, query head of the group), tokens first: the heads that share keys
+// share their expansion. Two tiles of 128 rows take turns on the tensor core
+// and in the softmax, over tiles of 128 keys:
+//   S = Q K^T (fp16; fp32 in tensor memory) -> softmax weights in registers,
+//   one thread a row -> P (bf16) back into S's tensor memory -> O += P V.
+// Roundings: a query row is bf16 values against the power of two above its
+// largest (fp16 has 11 bits for their 8), a key code x scale of at most 3 + 8
+// bits against the largest scale of its tile: both exact down to 2^-25 of that,
+// so the scores and the logarithm of the sum are as exact as fp32 sums. Values
+// are their codes (exact in bf16); a weight times its value's scale is rounded
+// to bf16 once (2^-8: fp16's range would not do, as rows that do not see a key
+// share its tile). Folding the value scales into the values instead, another
+// bf16 rounding, is cheaper in the softmax but made results a fourth worse.
+// Per pair of row tiles and key tile (D = 128) the tensor core needs 4 x 512
+// cycles, the 2 x 16384 exponentials 2048 at 16 a cycle, shared memory about
+// 2300 (operands 1536, expanded codes 512, scales 256): nothing has slack, so
+// each runs in warps of its own:
+//   warps 0-3, 4-7  softmax of row tile 0, 1 (also the final division)
+//   warps 8-11      codes -> bf16 operands in shared memory, swizzled for the
+//                   MMA; packed codes come straight from global memory into
+//                   registers, half a tile ahead
+//   warp 12         issues the MMAs
+// The running maximum may lag by a factor 2^8 (weights up to 256 in fp32 and
+// bf16 lose nothing): results in tensor memory are scaled anew only beyond.
+//
+// Few rows over a long cache are split along the keys, into parts that
+// kv4_prefill_join_kernel adds up in order.
+#include <algorithm>
+
+#include "kv4_common.cuh"
+#include "quant_core.cuh"
+#include "tc_common.cuh"
+
+#include <cuda_fp16.h>
+
+namespace tq {
+
+namespace {
+
+constexpr int kRows = 256, kKeys = 128;
+constexpr int kPrefillThreads = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kScaleSlots = 4;
+
+template <int D>
+struct PrefillShape {
+    // 128 rows or keys, bf16, in blocks of 64 values (rows of 128 bytes)
+    static constexpr int kTileBytes = 128 * D * 2;
+    static constexpr int kSmem = 6 * kTileBytes + 1024;  // 2 Q, 2 K, 2 V, alignment
+};
+
+struct PrefillParams {
+    Kv4View c;
+    Kv4Query q;
+    const int32_t *tok_start, *lens;
+    int T, rep, splits;
+    float *parts;  // [units][kv_heads][splits][256][D + 2] where splits > 1
+};
+
+// Unit (256 rows) `unit` of the call: its sequence, and where its rows begin.
+struct Unit {
+    int b;       // -1: none
+    int row0;    // of the sequence's n x rep rows
+    int start;   // the sequence's first token
+    int n;       // its tokens
+    int pos0;    // position of its first token
+};
+
+__device__ __forceinline__ int seq_tokens(const PrefillParams &p, int b, int *start)
+{
+    const int s = max(p.tok_start[b], 0), e = min(p.tok_start[b + 1], p.T);
+    *start = s;
+    return max(e - s, 0);
+}
+
+__device__ __forceinline__ int seq_units(const PrefillParams &p, int b)
+{
+    int s;
+    return b < p.c.batch ? (seq_tokens(p, b, &s) * p.rep + kRows - 1) / kRows : 0;
+}
+
+// The sequence that unit `u` counted from the call's last one belongs to: late
+// units of a prompt see most keys, so they start first.
+__device__ Unit find_unit(const PrefillParams &p, int u, int *scratch)
+{
+    const int threads = blockDim.x, warps = threads >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Unit r{-1, 0, 0, 0, 0};
+    int before = 0;  // units of the sequences behind the present block (from the back)
+    for (int b0 = 0; b0 < p.c.batch; b0 += threads) {
+        const int b = p.c.batch - 1 - b0 - int(threadIdx.x);
+        const int own = b >= 0 ? seq_units(p, b) : 0;
+        int incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        if (lane == 31)
+            scratch[warp] = incl;
+        __syncthreads();
+        int base = before;
+        for (int w = 0; w < warps; ++w) {
+            base += w < warp ? scratch[w] : 0;
+            before += scratch[w];
+        }
+        const int lo = base + incl - own;
+        if (u >= lo && u < lo + own) {
+            scratch[32] = b;
+            scratch[33] = own - 1 - (u - lo);
+        }
+        __syncthreads();
+        if (u < before) {
+            r.b = scratch[32];
+            r.row0 = scratch[33] * kRows;
+            break;
+        }
+    }
+    if (r.b >= 0) {
+        r.n = seq_tokens(p, r.b, &r.start);
+        r.pos0 = kv4_len(p.c, p.lens, r.b) - (p.tok_start[r.b + 1] - r.start);
+    }
+    return r;
+}
+
+// Key tiles [first, last) of 128 that a unit's split works through.
+struct Tiles {
+    int first, last;
+    int begin, end;  // keys that any row sees: [begin, end)
+};
+
+__device__ __forceinline__ Tiles tiles_of(const PrefillParams &p, const Unit &u, int split)
+{
+    const int last_row = min(u.row0 + kRows, u.n * p.rep) - 1;
+    const int p0 = u.pos0 + u.row0 / p.rep, p1 = u.pos0 + last_row / p.rep;
+    Tiles t;
+    t.end = min(max(p1 + 1, 0), p.c.max_len());
+    t.begin = p.q.window > 0 ? max(0, p0 - p.q.window + 1) : 0;
+    const int a = t.begin / kKeys, n = max(0, (t.end + kKeys - 1) / kKeys - a);
+    t.first = a + int((long long)n * split / p.splits);
+    t.last = a + int((long long)n * (split + 1) / p.splits);
+    return t;
+}
+
+// ------------------------------------------------------------- PTX wrappers
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool b_mn_major)
+{
+    return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) | (uint32_t(b_mn_major) << 16) |
+           (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// Operand whose rows of 64 values run along the MMA's N (values: N = elements,
+// K = keys): 8 keys are 1024 bytes apart, blocks of 64 values block_bytes.
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t block_bytes)
+{
+    uint64_t d = 0;
+    d |= uint64_t((saddr & 0x3FFFFu) >> 4);
+    d |= uint64_t(block_bytes >> 4) << 16;
+    d |= uint64_t(1024 >> 4) << 32;
+    d |= uint64_t(1) << 46;
+    d |= uint64_t(2) << 61;
+    return d;
+}
+
+// 32 columns of the thread's lane; the values are there after tmem_arrived().
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+          "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Ties the registers of an asynchronous load to the wait before this line: no
+// use of them can be moved above it.
+__device__ __forceinline__ void tmem_arrived(uint32_t *v)
+{
+    asm volatile("" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
+    asm volatile("" : "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]),
+                 "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]),
+                 "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]));
+}
+
+// Pairs of fp32 values in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <class T2>
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b)
+{
+    const T2 r = __hsub2(*reinterpret_cast<const T2 *>(&a), *reinterpret_cast<const T2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t c)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(c));
+    return r;
+}
+
+// A word of 8 nibbles n = code + 8 as 16-bit numbers, in the order 0 4 1 5 2 6
+// 3 7 in which the masks deliver them; the queries are stored in the same
+// order, and so come out the values' elements. Keys: under the exponent of
+// 1024 (64, one nibble higher) n is the fp16 number 1024 + n (64 + n), and the
+// code is multiplied by its scale. Values: under the exponent of 128 it is the
+// bf16 number 128 + n.
+__device__ __forceinline__ uint4 expand_keys(uint32_t w, uint32_t scale)
+{
+    const __half2 f = *reinterpret_cast<const __half2 *>(&scale);
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = i < 2 ? w : w >> 8;
+        r[i] = (i & 1) ? sub2<__half2>(and_or(x, 0x00F000F0u, 0x54005400u), 0x54805480u)
+                       : sub2<__half2>(and_or(x, 0x000F000Fu, 0x64006400u), 0x64086408u);
+        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&r[i]), f);
+        r[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+__device__ __forceinline__ uint4 expand_values(uint32_t w)
+{
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = sub2<__nv_bfloat162>(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u), 0x43084308u);
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// ------------------------------------------------------------------ kernel
+struct Bars {
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t scales[kScaleSlots];
+    uint64_t s_full[2], p_full[2], o_done[2];
+};
+
+struct Shared {
+    Bars bar;
+    float vs[kScaleSlots][kKeys];          // value scales
+    float unit[kScaleSlots];               // what 1 in the tile's key operand stands for
+    float row_unit[kRows];                 // and in a query row; NaN: a NaN or infinite query
+    uint4 skip[kScaleSlots];               // keys of pages outside the cache, a bit each
+    uint4 poison[kScaleSlots];             // keys whose value scale is NaN
+    uint32_t tmem;
+    int scratch[34];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPrefillThreads, 1)
+    kv4_prefill_kernel(const __grid_constant__ PrefillParams p)
+{
+    using S = PrefillShape<D>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared sh;
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *sq = smem, *sk = smem + 2 * S::kTileBytes, *sv = smem + 4 * S::kTileBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kvh = blockIdx.y, split = blockIdx.z;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.bar.k_full[i], 128);
+            mbar_init(&sh.bar.k_empty[i], 1);
+            mbar_init(&sh.bar.v_full[i], 128);
+            mbar_init(&sh.bar.v_empty[i], 1);
+            mbar_init(&sh.bar.s_full[i], 1);
+            mbar_init(&sh.bar.p_full[i], 128);
+            mbar_init(&sh.bar.o_done[i], 1);
+        }
+        for (int i = 0; i < kScaleSlots; ++i)
+            mbar_init(&sh.bar.scales[i], 128);
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    const Unit u = find_unit(p, blockIdx.x, sh.scratch);
+    if (u.b < 0)
+        return;
+    const Tiles tl = tiles_of(p, u, split);
+    const int n = tl.last - tl.first;
+    const int rows = min(kRows, u.n * p.rep - u.row0);
+    const int nq = rows > 128 ? 2 : 1;  // row tiles at work
+
+    if (n > 0) {
+        if (warp == 12)
+            tmem_alloc(&sh.tmem, 512);
+        // Queries: 16-byte chunks of 8 values, rows of a block 128 bytes apart,
+        // D / 8 neighbouring lanes a row.
+        for (int i = threadIdx.x; i < kRows * (D / 8); i += kPrefillThreads) {
+            const int r = i / (D / 8), ch = i - r * (D / 8);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < rows) {
+                const int tok = (u.row0 + r) / p.rep, h = (u.row0 + r) - tok * p.rep;
+                v = __ldg(reinterpret_cast<const uint4 *>(
+                    p.q.q + (u.start + tok) * p.q.q_stride +
+                    (long long)(kvh * p.rep + h) * D + ch * 8));
+            }
+            const float f[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
+                                bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                top = max(top, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int o = D / 16; o > 0; o >>= 1)
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int k = max(int(top >> 23) - 127, -100);
+            const float down = __uint_as_float(uint32_t(127 - min(k, 126)) << 23);
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __half2 x = __floats2half2_rn(f[e] * down, f[4 + e] * down);
+                w[e] = *reinterpret_cast<const uint32_t *>(&x);
+            }
+            *reinterpret_cast<uint4 *>(sq + (r >> 7) * S::kTileBytes + (ch >> 3) * 16384 +
+                                       sw128_off(r & 127, ch & 7)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+            if (ch == 0)
+                sh.row_unit[r] = top >= 0x7F800000u ? NAN : 1.0f / down;
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
+    const uint32_t tmem = n > 0 ? sh.tmem : 0;
+
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        // ---------------------------------------------------------- softmax
+        const int s = warp >> 2;
+        const int row = s * 128 + (warp & 3) * 32 + lane;
+        const int tok = (u.row0 + row) / p.rep, h = (u.row0 + row) - tok * p.rep;
+        const bool real = row < rows;
+        const int pos = real ? u.pos0 + tok : -1;
+        const int low = p.q.window > 0 ? pos - p.q.window + 1 : 0;  // first key seen
+        // what all rows of the tile see: keys [low_max, pos_min]
+        const int pos_min = u.pos0 + (u.row0 + s * 128) / p.rep;
+        const int last = min(s * 128 + 127, rows - 1);
+        const int low_max =
+            p.q.window > 0 ? u.pos0 + (u.row0 + last) / p.rep - p.q.window + 1 : 0;
+        const uint32_t lane_at = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lane_at + s * 128, to = tmem + lane_at + 256 + s * D;
+        const float row_mul = n > 0 ? sh.row_unit[row] * (p.q.scale * kLog2e) : 0.0f;
+        float m = -INFINITY, lsum = 0.0f;  // m: base 2, of scale x scores
+        bool poisoned = false, fine = s < nq;
+        for (int j = 0; j < n && fine; ++j) {
+            const int slot = j % kScaleSlots, j0 = (tl.first + j) * kKeys;
+            fine = mbar_wait_warp(&sh.bar.scales[slot], (j / kScaleSlots) & 1, p.c.err) &&
+                   mbar_wait_warp(&sh.bar.s_full[s], j & 1, p.c.err);
+            if (!fine)
+                break;
+            tc_fence_after();
+            uint32_t t[128];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tmem_ld32_async(ts + 32 * i, t + 32 * i);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tmem_arrived(t + 32 * i);
+            float mul = row_mul * sh.unit[slot];
+            if (mul < 1.17549435e-38f)  // (NaN stays) no zero, which masks would meet
+                mul = 1.17549435e-38f;
+            const uint4 sk4 = sh.skip[slot], po4 = sh.poison[slot];
+            const uint32_t skip[4] = {sk4.x, sk4.y, sk4.z, sk4.w};
+            const uint32_t poison[4] = {po4.x, po4.y, po4.z, po4.w};
+            const bool special = (sk4.x | sk4.y | sk4.z | sk4.w | po4.x | po4.y | po4.z | po4.w) != 0;
+            if (special || j0 + kKeys - 1 > pos_min || j0 < low_max) {
+                const int hi = pos - j0, lo = low - j0;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    // keys of these 32 that the row sees, a bit each
+                    uint32_t see = hi >= 32 * w + 31 ? 0xFFFFFFFFu
+                                   : hi < 32 * w     ? 0u
+                                                     : 0xFFFFFFFFu >> (31 - (hi - 32 * w));
+                    see &= lo <= 32 * w          ? 0xFFFFFFFFu
+                           : lo > 32 * w + 31 ? 0u
+                                              : 0xFFFFFFFFu << (lo - 32 * w);
+                    see &= ~skip[w];
+                    poisoned = poisoned || (see & poison[w]);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        t[32 * w + i] = (see >> i) & 1 ? t[32 * w + i] : 0xFF800000u;
+                }
+            }
+            float top[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                top[i] = fmaxf(__uint_as_float(t[32 * i]), __uint_as_float(t[32 * i + 1]));
+#pragma unroll
+                for (int k = 2; k < 32; k += 2)
+                    top[i] = fmaxf(top[i], fmaxf(__uint_as_float(t[32 * i + k]),
+                                                 __uint_as_float(t[32 * i + k + 1])));
+            }
+            const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mul;
+            if (m == -INFINITY) {
+                m = mt;  // nothing summed up yet
+            }
+            const bool grew = mt - m > 8.0f;
+            if (__any_sync(0xffffffffu, grew)) {
+                const float a = grew ? ex2(m - mt) : 1.0f;
+                if (grew)
+                    m = mt;
+                lsum *= a;
+                if (j > 0) {
+                    fine = mbar_wait_warp(&sh.bar.o_done[s], (j - 1) & 1, p.c.err);
+                    if (!fine)
+                        break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t o[32];
+                        tmem_ld32_async(to + 32 * i, o);
+                        tmem_ld_wait();
+                        tmem_arrived(o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                        tmem_st32_async(to + 32 * i, o);
+                    }
+                    tmem_st_wait();
+                }
+            }
+            const float neg = m == -INFINITY ? 0.0f : -m;
+            const float2 *vs = reinterpret_cast<const float2 *>(sh.vs[slot]);
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int k = half * 64 + 2 * i;
+                    float2 x = fma2(make_float2(__uint_as_float(t[k]), __uint_as_float(t[k + 1])),
+                                    make_float2(mul, mul), make_float2(neg, neg));
+                    x.x = ex2(x.x);
+                    x.y = ex2(x.y);
+                    sum[i & 1] = add2(sum[i & 1], x);
+                    x = mul2(x, vs[half * 32 + i]);
+                    pk[i] = pack_bf16(x.x, x.y);
+                }
+                tmem_st32_async(ts + 32 * half, pk);
+            }
+            lsum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sh.bar.p_full[s]);
+        }
+        // Output rows (a row tile without keys, or without rows, has none).
+        if (n > 0 && s < nq) {
+            fine = fine && mbar_wait_warp(&sh.bar.o_done[s], (n - 1) & 1, p.c.err);
+            tc_fence_after();
+        }
+        const float inv = lsum == 0.0f ? 0.0f : poisoned ? NAN : 1.0f / lsum;
+        const long long token = u.start + tok;
+        const int head = kvh * p.rep + h;
+        float *part = p.splits == 1
+                          ? nullptr
+                          : p.parts + ((((long long)blockIdx.x * p.c.kv_heads + kvh) * p.splits +
+                                        split) * kRows + row) * (D + 2);
+        if (s < nq) {
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32_async(to + 32 * i, o);
+                    tmem_ld_wait();
+                    tmem_arrived(o);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        o[k] = 0;
+                }
+                if (!real)
+                    continue;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float e[8];  // back from the order 0 4 1 5 2 6 3 7
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        e[k] = __uint_as_float(o[8 * c + 2 * k]);
+                        e[4 + k] = __uint_as_float(o[8 * c + 2 * k + 1]);
+                    }
+                    if (part) {
+#pragma unroll
+                        for (int k = 0; k < 8; k += 2)
+                            *reinterpret_cast<float2 *>(part + 32 * i + 8 * c + k) =
+                                poisoned ? make_float2(NAN, NAN)
+                                         : lsum == 0.0f ? make_float2(0.0f, 0.0f)
+                                                        : make_float2(e[k], e[k + 1]);
+                    } else {
+                        uint4 v;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            e[k] = lsum == 0.0f ? 0.0f : e[k] * inv;
+                        v.x = pack_bf16(e[0], e[1]);
+                        v.y = pack_bf16(e[2], e[3]);
+                        v.z = pack_bf16(e[4], e[5]);
+                        v.w = pack_bf16(e[6], e[7]);
+                        *reinterpret_cast<uint4 *>(p.q.out + token * p.q.out_stride +
+                                                   (long long)head * D + 32 * i + 8 * c) = v;
+                    }
+                }
+            }
+            if (real && part)
+                *reinterpret_cast<float2 *>(part + D) = make_float2(m, lsum);
+            else if (real && p.q.lse)
+                p.q.lse[token * p.q.q_heads + head] =
+                    lsum == 0.0f ? -INFINITY : (m + __log2f(lsum)) * kLn2;
+        }
+        tc_fence_before();
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        // ------------------------------------------------- codes to operands
+        // Thread i takes 16 bytes of codes of every kRowsAtOnce-th key. Lane l
+        // of each warp looks after the pages and scales of keys l, l + 32, ...
+        constexpr int kPerRow = D / 32, kRowsAtOnce = 128 / kPerRow, kSteps = 128 / kRowsAtOnce;
+        const int i = threadIdx.x - 256, w4 = warp - 8;
+        const int part = i % kPerRow, row0 = i / kPerRow;
+        const int ps = p.c.page_size(), mask = ps - 1;
+        const int32_t *table = p.c.table + (long long)u.b * p.c.max_pages;
+        const uint8_t *head = p.c.pages + kvh * p.c.template head_bytes<D>();
+        // Word w goes to chunk (part % 2) 4 + w of block part / 2; the two
+        // blocks of a row of 128 values take their words in another order, so
+        // that eight lanes' stores meet eight bank groups.
+        const int turn = D == 128 ? (part >> 1) * 2 : 0;
+        uint4 raw[2][kSteps];
+        int pg[4], next_pg[4] = {};   // pages of the lane's four keys: -1 not wanted, -2 bad
+        uint32_t ks[4], own_vs = 0;   // their key scales; key i's value scale
+        auto wanted = [&](int j) {
+            // (a page in front of a window may have gone to another sequence)
+            return j < tl.end && ((j >> p.c.lg_ps) + 1) << p.c.lg_ps > tl.begin;
+        };
+        auto pages = [&](int tile, int (&to)[4]) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int j = tile * kKeys + w * 32 + lane;
+                if (wanted(j))
+                    to[w] = table[j >> p.c.lg_ps];
+            }
+        };
+        auto block = [&](int page) { return head + (long long)page * p.c.page_stride; };
+        auto codes = [&](int tile, int which) {
+#pragma unroll
+            for (int r = 0; r < kSteps; ++r) {
+                const int key = r * kRowsAtOnce + row0, j = tile * kKeys + key;
+                const int from = D == 128 ? r : 2 * r + (w4 >> 1);  // key / 32, the same in a warp
+                const int page = __shfl_sync(0xffffffffu, from == 0 ? pg[0] : from == 1 ? pg[1]
+                                                          : from == 2 ? pg[2] : pg[3], key & 31);
+                raw[which][r] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                if (page >= 0)
+                    raw[which][r] = __ldg(reinterpret_cast<const uint4 *>(
+                        block(page) + (which * ps + (j & mask)) * (D / 2) + part * 16));
+            }
+        };
+        auto load_keys = [&](int tile) {  // their pages are in next_pg
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                pg[w] = wanted(tile * kKeys + w * 32 + lane) ? next_pg[w] : -1;
+                if (wanted(tile * kKeys + w * 32 + lane) &&
+                    unsigned(pg[w]) >= unsigned(p.c.num_pages)) {
+                    pg[w] = -2;
+                    atomicOr(p.c.err, kErrBadPage);
+                }
+            }
+            pages(tile + 1, next_pg);
+            codes(tile, 0);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                ks[w] = 0;
+                if (pg[w] >= 0) {
+                    const uint16_t *sc = reinterpret_cast<const uint16_t *>(block(pg[w]) + ps * D) +
+                                         ((tile * kKeys + w * 32 + lane) & mask);
+                    ks[w] = __ldg(sc);
+                    if (w == w4)
+                        own_vs = __ldg(sc + ps);
+                } else if (w == w4) {
+                    own_vs = 0;
+                }
+            }
+        };
+        auto store = [&](uint8_t *tile, int which, uint32_t (&scale)[4]) {
+#pragma unroll
+            for (int r = 0; r < kSteps; ++r) {
+                const int key = r * kRowsAtOnce + row0;
+                const int from = D == 128 ? r : 2 * r + (w4 >> 1);
+                uint32_t f = 0;
+                if (which == 0)
+                    f = __shfl_sync(0xffffffffu, from == 0 ? scale[0] : from == 1 ? scale[1]
+                                                 : from == 2 ? scale[2] : scale[3], key & 31);
+                uint4 x = raw[which][r];
+                if (turn)
+                    x = make_uint4(x.z, x.w, x.x, x.y);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint8_t *row = tile + (part >> 1) * 16384 + (key >> 3) * 1024 + (key & 7) * 128;
+                const int c0 = ((part & 1) * 4 + turn) ^ (key & 7);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<uint4 *>(row + ((c0 ^ q) << 4)) =
+                        which == 0 ? expand_keys(w[q], f) : expand_values(w[q]);
+            }
+        };
+        bool fine = true;
+        if (n > 0) {
+            pages(tl.first, next_pg);
+            load_keys(tl.first);
+            codes(tl.first, 1);
+        }
+        for (int j = 0; j < n && fine; ++j) {
+            const int st = j & 1, slot = j % kScaleSlots;
+            if (j >= 2)
+                fine = mbar_wait_warp(&sh.bar.k_empty[st], ((j >> 1) & 1) ^ 1, p.c.err);
+            if (!fine)
+                break;
+            // Key scales against the tile's largest (NaN and infinity aside),
+            // which becomes 2^11 .. 2^12: times 7 that is in fp16's range.
+            uint32_t top = 0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                top = max(top, (ks[w] & 0x7F80) == 0x7F80 ? 0u : ks[w] >> 7);
+            top = max(__reduce_max_sync(0xffffffffu, top), 13u);
+            uint32_t scale[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const __half h = __float2half_rn(__uint_as_float(ks[w] << 16) *
+                                                 __uint_as_float((265u - top) << 23));
+                const uint32_t b = __half_as_ushort(h);
+                scale[w] = b | b << 16;
+            }
+            store(sk + st * S::kTileBytes, 0, scale);
+            // A NaN value scale would reach, as 0 x NaN, rows that do not see
+            // the key: it is noted, and the rows that do see it find it there.
+            const uint32_t skip = __ballot_sync(
+                0xffffffffu, (w4 == 0 ? pg[0] : w4 == 1 ? pg[1] : w4 == 2 ? pg[2] : pg[3]) == -2);
+            const bool nan = (own_vs & 0x7F80) == 0x7F80;
+            const uint32_t poison = __ballot_sync(0xffffffffu, nan);
+            sh.vs[slot][i] = nan ? 0.0f : __uint_as_float(own_vs << 16);
+            if (lane == 0) {
+                reinterpret_cast<uint32_t *>(&sh.skip[slot])[w4] = skip;
+                reinterpret_cast<uint32_t *>(&sh.poison[slot])[w4] = poison;
+            }
+            if (i == 0)
+                sh.unit[slot] = __uint_as_float((top - 11u) << 23);
+            fence_proxy_async_smem();
+            mbar_arrive(&sh.bar.scales[slot]);
+            mbar_arrive(&sh.bar.k_full[st]);
+            // (values' pages are still those of tile j)
+            if (j >= 2)
+                fine = mbar_wait_warp(&sh.bar.v_empty[st], ((j >> 1) & 1) ^ 1, p.c.err);
+            if (!fine)
+                break;
+            if (j + 1 < n)
+                load_keys(tl.first + j + 1);
+            store(sv + st * S::kTileBytes, 1, scale);
+            fence_proxy_async_smem();
+            mbar_arrive(&sh.bar.v_full[st]);
+            if (j + 1 < n)
+                codes(tl.first + j + 1, 1);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+        // -------------------------------------------------------------- MMAs
+        if (warp == 12 && lane == 0 && n > 0) {
+            constexpr uint32_t kQk = idesc_f16(128, 128, false, false);
+            constexpr uint32_t kPv = idesc_f16(128, D, true, true);
+            const uint32_t q0 = smem_u32(sq), k0 = smem_u32(sk), v0 = smem_u32(sv);
+            auto scores = [&](int s, int st) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
+                    umma_f16(tmem + s * 128, umma_desc_sw128(q0 + s * S::kTileBytes + at),
+                              umma_desc_sw128(k0 + st * S::kTileBytes + at), kQk, k > 0);
+                }
+                umma_commit(&sh.bar.s_full[s]);
+            };
+            auto values = [&](int s, int st, bool first) {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                    umma_f16_ts(tmem + 256 + s * D, tmem + s * 128 + k * 8,
+                                 umma_desc_mn_sw128(v0 + st * S::kTileBytes + k * 2048, 16384),
+                                 kPv, !first || k > 0);
+                umma_commit(&sh.bar.o_done[s]);
+            };
+            bool fine = mbar_wait(&sh.bar.k_full[0], 0, p.c.err);
+            if (fine) {
+                tc_fence_after();
+                for (int s = 0; s < nq; ++s)
+                    scores(s, 0);
+                if (n > 2)
+                    umma_commit(&sh.bar.k_empty[0]);
+            }
+            for (int j = 0; j < n && fine; ++j) {
+                const int st = j & 1, parity = (j >> 1) & 1, nst = (j + 1) & 1;
+                fine = mbar_wait(&sh.bar.v_full[st], parity, p.c.err);
+                for (int s = 0; s < nq && fine; ++s) {
+                    fine = mbar_wait(&sh.bar.p_full[s], j & 1, p.c.err);
+                    if (!fine)
+                        break;
+                    tc_fence_after();
+                    values(s, st, j == 0);
+                    if (s == nq - 1 && j + 2 < n)  // (no arrival after the last wait)
+                        umma_commit(&sh.bar.v_empty[st]);
+                    if (j + 1 < n) {
+                        if (s == 0) {
+                            fine = mbar_wait(&sh.bar.k_full[nst], ((j + 1) >> 1) & 1, p.c.err);
+                            if (!fine)
+                                break;
+                            tc_fence_after();
+                        }
+                        scores(s, nst);
+                        if (s == nq - 1 && j + 3 < n)
+                            umma_commit(&sh.bar.k_empty[nst]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == 12 && n > 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Adds up the parts of a unit's rows, one warp a row at a time.
+constexpr int kJoinThreads = 256, kJoinRows = 32;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    kv4_prefill_join_kernel(const __grid_constant__ PrefillParams p)
+{
+    __shared__ int scratch[34];
+    pdl_wait();
+    pdl_launch_dependents();
+    const Unit u = find_unit(p, blockIdx.x, scratch);
+    if (u.b < 0)
+        return;
+    const int kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = min(kRows, u.n * p.rep - u.row0);
+    const float *unit = p.parts +
+                        ((long long)blockIdx.x * p.c.kv_heads + kvh) * p.splits * kRows * (D + 2);
+    for (int r = blockIdx.z * kJoinRows + warp; r < min(rows, int(blockIdx.z + 1) * kJoinRows);
+         r += kJoinThreads / 32) {
+        auto part = [&](int k) { return unit + ((long long)k * kRows + r) * (D + 2); };
+        // lane k: part k's maximum and sum
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (lane < p.splits)
+            ml = *reinterpret_cast<const float2 *>(part(lane) + D);
+        float m = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
+        float l = w * ml.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            l += __shfl_xor_sync(0xffffffffu, l, o);
+        float2 v[D / 64] = {};
+        for (int k = 0; k < p.splits; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const float2 x = *reinterpret_cast<const float2 *>(part(k) + i * 64 + 2 * lane);
+                v[i].x = fmaf(wk, x.x, v[i].x);
+                v[i].y = fmaf(wk, x.y, v[i].y);
+            }
+        }
+        const int tok = (u.row0 + r) / p.rep, h = (u.row0 + r) - tok * p.rep;
+        const long long token = u.start + tok;
+        const int head = kvh * p.rep + h;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+            *reinterpret_cast<uint32_t *>(p.q.out + token * p.q.out_stride + (long long)head * D +
+                                          i * 64 + 2 * lane) = pack_bf16(v[i].x * inv, v[i].y * inv);
+        if (p.q.lse && lane == 0)
+            p.q.lse[token * p.q.q_heads + head] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    }
+}
+
+struct PrefillPlan {
+    int rep, units, splits;
+    size_t bytes;
+};
+
+// Units at most (rows fill them but for one per sequence), and parts per unit.
+// CTAs run one to an SM, so s parts of c units' tiles take ceil(c s / SMs)
+// turns of tiles / s each, and about four tiles' time for every turn's start,
+// end and joining; from two turns on, parts gain less than they cost.
+PrefillPlan plan_prefill(const Kv4View &c, int D, int q_heads, int T)
+{
+    PrefillPlan d;
+    d.rep = q_heads / c.kv_heads;
+    const long long rows = (long long)T * d.rep;
+    const long long units = rows / kRows + std::min(c.batch, T);
+    d.units = int(std::min<long long>(units, INT32_MAX));
+    const int sms = device_sm_count();
+    const long long ctas =
+        std::max<long long>((rows + kRows - 1) / kRows, std::min(c.batch, T)) * c.kv_heads;
+    const int tiles = (c.max_len() + kKeys - 1) / kKeys;
+    d.splits = 1;
+    double best = 1e30;
+    for (int s = 1; s <= 32 && s <= std::max(1, tiles); ++s) {
+        if (s > 1 && ctas >= 2ll * sms)
+            break;
+        const double turns = double((ctas * s + sms - 1) / sms);
+        const double cost = turns * (double(tiles) / s + 4.0) + (s > 1 ? 4.0 : 0.0);
+        if (cost < best) {
+            best = cost;
+            d.splits = s;
+        }
+    }
+    d.bytes = d.splits == 1 ? 0
+                            : size_t(d.units) * c.kv_heads * d.splits * kRows * size_t(D + 2) *
+                                  sizeof(float);
+    return d;
+}
+
+template <int D>
+cudaError_t launch(const PrefillParams &p, const PrefillPlan &plan, cudaStream_t stream)
+{
+    using S = PrefillShape<D>;
+    static thread_local int configured_dev = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && configured_dev != dev) {
+        e = cudaFuncSetAttribute(kv4_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 S::kSmem);
+        if (e == cudaSuccess)
+            configured_dev = dev;
+    }
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3(unsigned(plan.units), unsigned(p.c.kv_heads), unsigned(plan.splits));
+    cfg.blockDim = dim3(kPrefillThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    e = cudaLaunchKernelEx(&cfg, kv4_prefill_kernel<D>, p);
+    if (e != cudaSuccess || plan.splits == 1)
+        return e;
+    cfg.gridDim = dim3(unsigned(plan.units), unsigned(p.c.kv_heads), kRows / kJoinRows);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, kv4_prefill_join_kernel<D>, p);
+}
+
+}  // namespace
+
+size_t kv4_prefill_workspace(const Kv4View &c, int D, int q_heads, int T)
+{
+    return c.batch > 0 && T > 0 ? plan_prefill(c, D, q_heads, T).bytes : 0;
+}
+
+cudaError_t launch_kv4_prefill(const Kv4View &c, int D, const Kv4Query &q,
+                               const int32_t *tok_start, const int32_t *lens, int T,
+                               void *workspace, cudaStream_t stream)
+{
+    const PrefillPlan plan = plan_prefill(c, D, q.q_heads, T);
+    if ((long long)T * plan.rep > INT32_MAX - kRows)
+        return cudaErrorInvalidValue;  // rows are counted in 32 bits
+    PrefillParams p;
+    p.c = c;
+    p.q = q;
+    p.tok_start = tok_start;
+    p.lens = lens;
+    p.T = T;
+    p.rep = plan.rep;
+    p.splits = plan.splits;
+    p.parts = static_cast<float *>(workspace);
+    return D == 128 ? launch<128>(p, plan, stream) : launch<64>(p, plan, stream);
+}
+
+}  // namespace tq

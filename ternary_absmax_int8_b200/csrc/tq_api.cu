@@ -673,7 +673,7 @@ tq_status tq_kv4_prefill_workspace(const tq_kv4_cache *cache, int q_heads, int T
         return fail(TQ_ERR_SHAPE, "%s: T=%d", fn, T);
     if (!bytes)
         return fail(TQ_ERR_NULL, "%s: bytes is NULL", fn);
-    *bytes = 0;
+    *bytes = tq::kv4_prefill_workspace(c, cache->head_dim, q_heads, T);
     return ok();
 }
 
@@ -729,7 +729,8 @@ tq_status tq_kv4_prefill(const tq_kv4_cache *cache, const tq_kv4_query *query,
         return fail(TQ_ERR_ALIGN, "%s: lens and tok_start must be 4-byte aligned", fn);
     if ((st = kv4_error_word(fn, &c)) != TQ_OK)
         return st;
-    cudaError_t e = tq::launch_kv4_attn(c, cache->head_dim, q, tok_start, lens, T, stream);
+    cudaError_t e = tq::launch_kv4_prefill(c, cache->head_dim, q, tok_start, lens, T, workspace,
+                                           stream);
     return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }
 

@@ -324,8 +324,10 @@ cudaError_t launch_kv4_append(const Kv4View &c, int D, const void *k, const void
 size_t kv4_decode_workspace(const Kv4View &c, int D, int q_heads);
 cudaError_t launch_kv4_decode(const Kv4View &c, int D, const Kv4Query &q, const int32_t *lens,
                               void *workspace, cudaStream_t stream);
-cudaError_t launch_kv4_attn(const Kv4View &c, int D, const Kv4Query &q, const int32_t *tok_start,
-                            const int32_t *lens, int T, cudaStream_t stream);
+size_t kv4_prefill_workspace(const Kv4View &c, int D, int q_heads, int T);
+cudaError_t launch_kv4_prefill(const Kv4View &c, int D, const Kv4Query &q,
+                               const int32_t *tok_start, const int32_t *lens, int T,
+                               void *workspace, cudaStream_t stream);
 
 // Device address of the library's error word on the current device.
 unsigned *device_error_word();
