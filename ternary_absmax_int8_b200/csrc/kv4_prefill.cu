@@ -20,10 +20,10 @@
 // 2300 (operands 1536, expanded codes 512, scales 256): nothing has slack, so
 // each runs in warps of its own:
 //   warps 0-3, 4-7  softmax of row tile 0, 1 (also the final division)
-//   warps 8-11      codes -> bf16 operands in shared memory, swizzled for the
-//                   MMA; packed codes come straight from global memory into
-//                   registers, half a tile ahead
+//   warps 8-11      codes -> 16-bit operands, swizzled for the MMA
 //   warp 12         issues the MMAs
+//   warp 13         looks up pages and issues bulk copies of packed codes, two
+//                   tiles ahead
 // The running maximum may lag by a factor 2^8 (weights up to 256 in fp32 and
 // bf16 lose nothing): results in tensor memory are scaled anew only beyond.
 //
@@ -45,13 +45,13 @@ constexpr int kRows = 256, kKeys = 128;
 constexpr int kPrefillThreads = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kScaleSlots = 4;
+constexpr int kScaleSlots = 3;
 
 template <int D>
 struct PrefillShape {
     // 128 rows or keys, bf16, in blocks of 64 values (rows of 128 bytes)
     static constexpr int kTileBytes = 128 * D * 2;
-    static constexpr int kSmem = 6 * kTileBytes + 1024;  // 2 Q, 2 K, 2 V, alignment
+    static constexpr int kPacked = 128 * D / 2;  // a tile's key or value codes
 };
 
 struct PrefillParams {
@@ -149,6 +149,15 @@ __device__ __forceinline__ Tiles tiles_of(const PrefillParams &p, const Unit &u,
 }
 
 // ------------------------------------------------------------- PTX wrappers
+// Bulk copy with L2's own policy: other CTAs of the sequence read the same codes.
+__device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool b_mn_major)
 {
     return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) | (uint32_t(b_mn_major) << 16) |
@@ -173,6 +182,14 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
                  "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
                  : "memory");
+}
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(p));
+    return p != 0;
 }
 
 // Operand whose rows of 64 values run along the MMA's N (values: N = elements,
@@ -305,17 +322,28 @@ struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t scales[kScaleSlots];
     uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t packed_full[2][2], packed_empty[2][2];  // [keys, values][stage]
 };
 
+// Shared memory. Operand tiles stand on 1024 bytes (the swizzle's period):
+// the struct is all of the kernel's shared memory, which begins there.
+template <int D>
 struct Shared {
-    Bars bar;
-    float vs[kScaleSlots][kKeys];          // value scales
-    float unit[kScaleSlots];               // what 1 in the tile's key operand stands for
-    float row_unit[kRows];                 // and in a query row; NaN: a NaN or infinite query
-    uint4 skip[kScaleSlots];               // keys of pages outside the cache, a bit each
-    uint4 poison[kScaleSlots];             // keys whose value scale is NaN
+    uint8_t q[2][PrefillShape<D>::kTileBytes];
+    uint8_t k[2][PrefillShape<D>::kTileBytes];
+    uint8_t v[2][PrefillShape<D>::kTileBytes];
+    uint8_t packed[2][2][PrefillShape<D>::kPacked];  // [keys, values][stage] codes
+    uint16_t scales[2][2][kKeys];                    // [stage][keys, values] as stored
+    float vs[kScaleSlots][kKeys];                    // value scales
+    uint4 skip[kScaleSlots];    // keys of pages outside the cache, a bit each
+    uint4 poison[kScaleSlots];  // keys whose value scale is NaN
+    float unit[kScaleSlots];    // what 1 in the tile's key operand stands for
+    uint32_t pages[2];          // [stage] pages that are there, and << 16 bad ones
     uint32_t tmem;
-    int scratch[34];
+    Bars bar;
+    // only until the roles part:
+    __device__ __forceinline__ float *row_unit() { return reinterpret_cast<float *>(v[1]); }
+    __device__ __forceinline__ int *scratch() { return reinterpret_cast<int *>(v[0]); }
 };
 
 template <int D>
@@ -323,10 +351,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     kv4_prefill_kernel(const __grid_constant__ PrefillParams p)
 {
     using S = PrefillShape<D>;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ Shared sh;
-    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t *sq = smem, *sk = smem + 2 * S::kTileBytes, *sv = smem + 4 * S::kTileBytes;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Shared<D> &sh = *reinterpret_cast<Shared<D> *>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kvh = blockIdx.y, split = blockIdx.z;
 
@@ -339,6 +365,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             mbar_init(&sh.bar.s_full[i], 1);
             mbar_init(&sh.bar.p_full[i], 128);
             mbar_init(&sh.bar.o_done[i], 1);
+            for (int w = 0; w < 2; ++w) {
+                mbar_init(&sh.bar.packed_full[w][i], 1);
+                mbar_init(&sh.bar.packed_empty[w][i], 4);
+            }
         }
         for (int i = 0; i < kScaleSlots; ++i)
             mbar_init(&sh.bar.scales[i], 128);
@@ -346,7 +376,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     }
     pdl_wait();
     pdl_launch_dependents();
-    const Unit u = find_unit(p, blockIdx.x, sh.scratch);
+    const Unit u = find_unit(p, blockIdx.x, sh.scratch());
     if (u.b < 0)
         return;
     const Tiles tl = tiles_of(p, u, split);
@@ -385,11 +415,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                 const __half2 x = __floats2half2_rn(f[e] * down, f[4 + e] * down);
                 w[e] = *reinterpret_cast<const uint32_t *>(&x);
             }
-            *reinterpret_cast<uint4 *>(sq + (r >> 7) * S::kTileBytes + (ch >> 3) * 16384 +
+            *reinterpret_cast<uint4 *>(sh.q[r >> 7] + (ch >> 3) * 16384 +
                                        sw128_off(r & 127, ch & 7)) =
                 make_uint4(w[0], w[1], w[2], w[3]);
             if (ch == 0)
-                sh.row_unit[r] = top >= 0x7F800000u ? NAN : 1.0f / down;
+                sh.row_unit()[r] = top >= 0x7F800000u ? NAN : 1.0f / down;
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -397,6 +427,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         tc_fence_after();
     }
     const uint32_t tmem = n > 0 ? sh.tmem : 0;
+    float row_mul = 0.0f;
+    if (n > 0) {
+        if (warp < 8)
+            row_mul = sh.row_unit()[threadIdx.x] * (p.q.scale * kLog2e);
+        __syncthreads();
+    }
 
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
@@ -414,7 +450,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             p.q.window > 0 ? u.pos0 + (u.row0 + last) / p.rep - p.q.window + 1 : 0;
         const uint32_t lane_at = uint32_t((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_at + s * 128, to = tmem + lane_at + 256 + s * D;
-        const float row_mul = n > 0 ? sh.row_unit[row] * (p.q.scale * kLog2e) : 0.0f;
         float m = -INFINITY, lsum = 0.0f;  // m: base 2, of scale x scores
         bool poisoned = false, fine = s < nq;
         for (int j = 0; j < n && fine; ++j) {
@@ -583,85 +618,28 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         }
         tc_fence_before();
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         // ------------------------------------------------- codes to operands
         // Thread i takes 16 bytes of codes of every kRowsAtOnce-th key. Lane l
-        // of each warp looks after the pages and scales of keys l, l + 32, ...
+        // of each warp looks after the scales of keys l, l + 32, ...
         constexpr int kPerRow = D / 32, kRowsAtOnce = 128 / kPerRow, kSteps = 128 / kRowsAtOnce;
         const int i = threadIdx.x - 256, w4 = warp - 8;
         const int part = i % kPerRow, row0 = i / kPerRow;
-        const int ps = p.c.page_size(), mask = ps - 1;
-        const int32_t *table = p.c.table + (long long)u.b * p.c.max_pages;
-        const uint8_t *head = p.c.pages + kvh * p.c.template head_bytes<D>();
         // Word w goes to chunk (part % 2) 4 + w of block part / 2; the two
         // blocks of a row of 128 values take their words in another order, so
         // that eight lanes' stores meet eight bank groups.
         const int turn = D == 128 ? (part >> 1) * 2 : 0;
-        uint4 raw[2][kSteps];
-        int pg[4], next_pg[4] = {};   // pages of the lane's four keys: -1 not wanted, -2 bad
-        uint32_t ks[4], own_vs = 0;   // their key scales; key i's value scale
-        auto wanted = [&](int j) {
-            // (a page in front of a window may have gone to another sequence)
-            return j < tl.end && ((j >> p.c.lg_ps) + 1) << p.c.lg_ps > tl.begin;
-        };
-        auto pages = [&](int tile, int (&to)[4]) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int j = tile * kKeys + w * 32 + lane;
-                if (wanted(j))
-                    to[w] = table[j >> p.c.lg_ps];
-            }
-        };
-        auto block = [&](int page) { return head + (long long)page * p.c.page_stride; };
-        auto codes = [&](int tile, int which) {
-#pragma unroll
-            for (int r = 0; r < kSteps; ++r) {
-                const int key = r * kRowsAtOnce + row0, j = tile * kKeys + key;
-                const int from = D == 128 ? r : 2 * r + (w4 >> 1);  // key / 32, the same in a warp
-                const int page = __shfl_sync(0xffffffffu, from == 0 ? pg[0] : from == 1 ? pg[1]
-                                                          : from == 2 ? pg[2] : pg[3], key & 31);
-                raw[which][r] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                if (page >= 0)
-                    raw[which][r] = __ldg(reinterpret_cast<const uint4 *>(
-                        block(page) + (which * ps + (j & mask)) * (D / 2) + part * 16));
-            }
-        };
-        auto load_keys = [&](int tile) {  // their pages are in next_pg
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                pg[w] = wanted(tile * kKeys + w * 32 + lane) ? next_pg[w] : -1;
-                if (wanted(tile * kKeys + w * 32 + lane) &&
-                    unsigned(pg[w]) >= unsigned(p.c.num_pages)) {
-                    pg[w] = -2;
-                    atomicOr(p.c.err, kErrBadPage);
-                }
-            }
-            pages(tile + 1, next_pg);
-            codes(tile, 0);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                ks[w] = 0;
-                if (pg[w] >= 0) {
-                    const uint16_t *sc = reinterpret_cast<const uint16_t *>(block(pg[w]) + ps * D) +
-                                         ((tile * kKeys + w * 32 + lane) & mask);
-                    ks[w] = __ldg(sc);
-                    if (w == w4)
-                        own_vs = __ldg(sc + ps);
-                } else if (w == w4) {
-                    own_vs = 0;
-                }
-            }
-        };
-        auto store = [&](uint8_t *tile, int which, uint32_t (&scale)[4]) {
+        auto expand = [&](uint8_t *tile, const uint8_t *packed, bool keys, const uint32_t *scale) {
 #pragma unroll
             for (int r = 0; r < kSteps; ++r) {
                 const int key = r * kRowsAtOnce + row0;
-                const int from = D == 128 ? r : 2 * r + (w4 >> 1);
                 uint32_t f = 0;
-                if (which == 0)
+                if (keys) {
+                    const int from = D == 128 ? r : 2 * r + (w4 >> 1);  // key / 32, the warp's
                     f = __shfl_sync(0xffffffffu, from == 0 ? scale[0] : from == 1 ? scale[1]
                                                  : from == 2 ? scale[2] : scale[3], key & 31);
-                uint4 x = raw[which][r];
+                }
+                uint4 x = lds128(packed + (r * 128 + i) * 16);
                 if (turn)
                     x = make_uint4(x.z, x.w, x.x, x.y);
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -670,27 +648,29 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     *reinterpret_cast<uint4 *>(row + ((c0 ^ q) << 4)) =
-                        which == 0 ? expand_keys(w[q], f) : expand_values(w[q]);
+                        keys ? expand_keys(w[q], f) : expand_values(w[q]);
             }
         };
         bool fine = true;
-        if (n > 0) {
-            pages(tl.first, next_pg);
-            load_keys(tl.first);
-            codes(tl.first, 1);
-        }
-        for (int j = 0; j < n && fine; ++j) {
-            const int st = j & 1, slot = j % kScaleSlots;
-            if (j >= 2)
-                fine = mbar_wait_warp(&sh.bar.k_empty[st], ((j >> 1) & 1) ^ 1, p.c.err);
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+            const int st = j & 1, slot = j % kScaleSlots, parity = (j >> 1) & 1;
+            fine = (j < 2 || mbar_wait_warp(&sh.bar.k_empty[st], parity ^ 1, p.c.err)) &&
+                   mbar_wait_warp(&sh.bar.packed_full[0][st], parity, p.c.err);
             if (!fine)
                 break;
             // Key scales against the tile's largest (NaN and infinity aside),
-            // which becomes 2^11 .. 2^12: times 7 that is in fp16's range.
-            uint32_t top = 0;
+            // which becomes 2^11 .. 2^12: times 7 that is in fp16's range. Keys
+            // that no row sees, or that are not there, have scale 0.
+            const uint32_t pages = sh.pages[st];
+            uint32_t ks[4], top = 0;
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
+            for (int w = 0; w < 4; ++w) {
+                const int key = w * 32 + lane, at = (tl.first + j) * kKeys + key;
+                const bool in = at >= tl.begin && at < tl.end && (pages >> (key >> p.c.lg_ps) & 1);
+                ks[w] = in ? sh.scales[st][0][key] : 0u;
                 top = max(top, (ks[w] & 0x7F80) == 0x7F80 ? 0u : ks[w] >> 7);
+            }
             top = max(__reduce_max_sync(0xffffffffu, top), 13u);
             uint32_t scale[4];
 #pragma unroll
@@ -700,91 +680,171 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                 const uint32_t b = __half_as_ushort(h);
                 scale[w] = b | b << 16;
             }
-            store(sk + st * S::kTileBytes, 0, scale);
             // A NaN value scale would reach, as 0 x NaN, rows that do not see
             // the key: it is noted, and the rows that do see it find it there.
-            const uint32_t skip = __ballot_sync(
-                0xffffffffu, (w4 == 0 ? pg[0] : w4 == 1 ? pg[1] : w4 == 2 ? pg[2] : pg[3]) == -2);
-            const bool nan = (own_vs & 0x7F80) == 0x7F80;
+            const int own = (tl.first + j) * kKeys + i;
+            const bool in = own >= tl.begin && own < tl.end && (pages >> (i >> p.c.lg_ps) & 1);
+            const uint32_t vs = in ? sh.scales[st][1][i] : 0u;
+            const uint32_t skip =
+                __ballot_sync(0xffffffffu, (pages >> (16 + (i >> p.c.lg_ps))) & 1);
+            const bool nan = (vs & 0x7F80) == 0x7F80;
             const uint32_t poison = __ballot_sync(0xffffffffu, nan);
-            sh.vs[slot][i] = nan ? 0.0f : __uint_as_float(own_vs << 16);
+            sh.vs[slot][i] = nan ? 0.0f : __uint_as_float(vs << 16);
             if (lane == 0) {
                 reinterpret_cast<uint32_t *>(&sh.skip[slot])[w4] = skip;
                 reinterpret_cast<uint32_t *>(&sh.poison[slot])[w4] = poison;
             }
             if (i == 0)
                 sh.unit[slot] = __uint_as_float((top - 11u) << 23);
-            fence_proxy_async_smem();
             mbar_arrive(&sh.bar.scales[slot]);
+            expand(sh.k[st], sh.packed[0][st], true, scale);
+            fence_proxy_async_smem();
             mbar_arrive(&sh.bar.k_full[st]);
-            // (values' pages are still those of tile j)
-            if (j >= 2)
-                fine = mbar_wait_warp(&sh.bar.v_empty[st], ((j >> 1) & 1) ^ 1, p.c.err);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.bar.packed_empty[0][st]);
+            fine = (j < 2 || mbar_wait_warp(&sh.bar.v_empty[st], parity ^ 1, p.c.err)) &&
+                   mbar_wait_warp(&sh.bar.packed_full[1][st], parity, p.c.err);
             if (!fine)
                 break;
-            if (j + 1 < n)
-                load_keys(tl.first + j + 1);
-            store(sv + st * S::kTileBytes, 1, scale);
+            expand(sh.v[st], sh.packed[1][st], false, scale);
             fence_proxy_async_smem();
             mbar_arrive(&sh.bar.v_full[st]);
-            if (j + 1 < n)
-                codes(tl.first + j + 1, 1);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.bar.packed_empty[1][st]);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         // -------------------------------------------------------------- MMAs
-        if (warp == 12 && lane == 0 && n > 0) {
+        // The whole warp walks the loop, so that addresses and descriptors stay
+        // in uniform registers; one elected lane issues (issue by a lone lane of
+        // a divergent branch took 100 cycles a product, twice its execution).
+        if (warp == 12 && n > 0) {
             constexpr uint32_t kQk = idesc_f16(128, 128, false, false);
             constexpr uint32_t kPv = idesc_f16(128, D, true, true);
-            const uint32_t q0 = smem_u32(sq), k0 = smem_u32(sk), v0 = smem_u32(sv);
+            const uint64_t q0 = umma_desc_sw128(smem_u32(sh.q)), k0 = umma_desc_sw128(smem_u32(sh.k));
+            const uint64_t v0 = umma_desc_mn_sw128(smem_u32(sh.v), 16384);
+            const bool lead = elect_one();
             auto scores = [&](int s, int st) {
+                const uint64_t a = umma_desc_advance(q0, s * S::kTileBytes);
+                const uint64_t b = umma_desc_advance(k0, st * S::kTileBytes);
+                if (lead) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
-                    umma_f16(tmem + s * 128, umma_desc_sw128(q0 + s * S::kTileBytes + at),
-                              umma_desc_sw128(k0 + st * S::kTileBytes + at), kQk, k > 0);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
+                        umma_f16(tmem + s * 128, umma_desc_advance(a, at), umma_desc_advance(b, at),
+                                 kQk, k > 0);
+                    }
+                    umma_commit(&sh.bar.s_full[s]);
                 }
-                umma_commit(&sh.bar.s_full[s]);
             };
             auto values = [&](int s, int st, bool first) {
+                const uint64_t b = umma_desc_advance(v0, st * S::kTileBytes);
+                if (lead) {
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    umma_f16_ts(tmem + 256 + s * D, tmem + s * 128 + k * 8,
-                                 umma_desc_mn_sw128(v0 + st * S::kTileBytes + k * 2048, 16384),
-                                 kPv, !first || k > 0);
-                umma_commit(&sh.bar.o_done[s]);
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        umma_f16_ts(tmem + 256 + s * D, tmem + s * 128 + k * 8,
+                                    umma_desc_advance(b, k * 2048), kPv, !first || k > 0);
+                    umma_commit(&sh.bar.o_done[s]);
+                }
             };
-            bool fine = mbar_wait(&sh.bar.k_full[0], 0, p.c.err);
+            bool fine = mbar_wait_warp(&sh.bar.k_full[0], 0, p.c.err);
             if (fine) {
                 tc_fence_after();
                 for (int s = 0; s < nq; ++s)
                     scores(s, 0);
-                if (n > 2)
+                if (n > 2 && lead)
                     umma_commit(&sh.bar.k_empty[0]);
             }
+#pragma unroll 1
             for (int j = 0; j < n && fine; ++j) {
                 const int st = j & 1, parity = (j >> 1) & 1, nst = (j + 1) & 1;
-                fine = mbar_wait(&sh.bar.v_full[st], parity, p.c.err);
-                for (int s = 0; s < nq && fine; ++s) {
-                    fine = mbar_wait(&sh.bar.p_full[s], j & 1, p.c.err);
+                fine = mbar_wait_warp(&sh.bar.v_full[st], parity, p.c.err);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (s >= nq || !fine)
+                        break;
+                    fine = mbar_wait_warp(&sh.bar.p_full[s], j & 1, p.c.err);
                     if (!fine)
                         break;
                     tc_fence_after();
                     values(s, st, j == 0);
-                    if (s == nq - 1 && j + 2 < n)  // (no arrival after the last wait)
+                    if (s == nq - 1 && j + 2 < n && lead)  // (no arrival after the last wait)
                         umma_commit(&sh.bar.v_empty[st]);
                     if (j + 1 < n) {
                         if (s == 0) {
-                            fine = mbar_wait(&sh.bar.k_full[nst], ((j + 1) >> 1) & 1, p.c.err);
+                            fine = mbar_wait_warp(&sh.bar.k_full[nst], ((j + 1) >> 1) & 1, p.c.err);
                             if (!fine)
                                 break;
                             tc_fence_after();
                         }
                         scores(s, nst);
-                        if (s == nq - 1 && j + 3 < n)
+                        if (s == nq - 1 && j + 3 < n && lead)
                             umma_commit(&sh.bar.k_empty[nst]);
                     }
                 }
+            }
+        }
+        // ------------------------------------------------------------ copies
+        if (warp == 13) {
+            // Lane 4 g + w: page g of a tile; w: its key codes, value codes, key
+            // scales, value scales.
+            const int ps = p.c.page_size(), per_tile = kKeys >> p.c.lg_ps;
+            const int g = lane >> 2, w = lane & 3;
+            const int32_t *table = p.c.table + (long long)u.b * p.c.max_pages;
+            const uint8_t *head = p.c.pages + kvh * p.c.template head_bytes<D>();
+            const long long off = w < 2 ? (long long)w * ps * (D / 2)
+                                        : (long long)ps * D + (w - 2) * 2 * ps;
+            auto wanted = [&](int tile) {
+                const int index = tile * per_tile + g;
+                // (a page in front of a window may have gone to another sequence)
+                return g < per_tile && index << p.c.lg_ps < tl.end &&
+                       (index + 1) << p.c.lg_ps > tl.begin;
+            };
+            auto page_of = [&](int tile) { return wanted(tile) ? table[tile * per_tile + g] : 0; };
+            int next = n > 0 ? page_of(tl.first) : 0;
+            bool fine = true;
+#pragma unroll 1
+            for (int j = 0; j < n; ++j) {
+                const int st = j & 1, parity = ((j >> 1) & 1) ^ 1, page = next;
+                if (j + 1 < n)
+                    next = page_of(tl.first + j + 1);
+                const bool want = wanted(tl.first + j);
+                const bool bad = want && unsigned(page) >= unsigned(p.c.num_pages);
+                const uint32_t there = __ballot_sync(0xffffffffu, want && !bad && w == 0);
+                const uint32_t wrong = __ballot_sync(0xffffffffu, bad && w == 0);
+                const uint8_t *src = head + (long long)page * p.c.page_stride + off;
+                fine = (j < 2 || mbar_wait_warp(&sh.bar.packed_empty[0][st], parity, p.c.err));
+                if (!fine)
+                    break;
+                if (lane == 0) {
+                    uint32_t a = 0, b = 0;  // a bit a page
+                    for (int k = 0; k < 8; ++k) {
+                        a |= (there >> (4 * k) & 1) << k;
+                        b |= (wrong >> (4 * k) & 1) << k;
+                    }
+                    if (b)
+                        atomicOr(p.c.err, kErrBadPage);
+                    sh.pages[st] = a | b << 16;
+                    mbar_arrive_expect_tx(&sh.bar.packed_full[0][st],
+                                          __popc(there) * uint32_t(ps) * (D / 2 + 4));
+                }
+                __syncwarp();
+                if (want && !bad && w != 1)
+                    bulk_copy(w == 0 ? sh.packed[0][st] + g * ps * (D / 2)
+                                    : reinterpret_cast<uint8_t *>(&sh.scales[st][w - 2][g * ps]),
+                             src, w == 0 ? ps * (D / 2) : ps * 2, &sh.bar.packed_full[0][st]);
+                fine = (j < 2 || mbar_wait_warp(&sh.bar.packed_empty[1][st], parity, p.c.err));
+                if (!fine)
+                    break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&sh.bar.packed_full[1][st],
+                                          __popc(there) * uint32_t(ps) * (D / 2));
+                __syncwarp();
+                if (want && !bad && w == 1)
+                    bulk_copy(sh.packed[1][st] + g * ps * (D / 2), src, ps * (D / 2),
+                              &sh.bar.packed_full[1][st]);
             }
         }
         __syncwarp();
@@ -899,7 +959,7 @@ cudaError_t launch(const PrefillParams &p, const PrefillPlan &plan, cudaStream_t
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && configured_dev != dev) {
         e = cudaFuncSetAttribute(kv4_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 S::kSmem);
+                                 int(sizeof(Shared<D>)));
         if (e == cudaSuccess)
             configured_dev = dev;
     }
@@ -914,7 +974,7 @@ cudaError_t launch(const PrefillParams &p, const PrefillPlan &plan, cudaStream_t
     cfg.stream = stream;
     cfg.gridDim = dim3(unsigned(plan.units), unsigned(p.c.kv_heads), unsigned(plan.splits));
     cfg.blockDim = dim3(kPrefillThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.dynamicSmemBytes = int(sizeof(Shared<D>));
     e = cudaLaunchKernelEx(&cfg, kv4_prefill_kernel<D>, p);
     if (e != cudaSuccess || plan.splits == 1)
         return e;
