@@ -21,7 +21,7 @@
 // each runs in warps of its own:
 //   warps 0-3, 4-7  softmax of row tile 0, 1 (also the final division)
 //   warps 8-11      codes -> 16-bit operands, swizzled for the MMA
-//   warp 12         issues the MMAs
+//   warps 12, 14    issue the MMAs of row tile 0, 1
 //   warp 13         looks up pages and issues bulk copies of packed codes, two
 //                   tiles ahead
 // The running maximum may lag by a factor 2^8 (weights up to 256 in fp32 and
@@ -41,7 +41,7 @@ namespace tq {
 
 namespace {
 
-constexpr int kRows = 256, kKeys = 128;
+constexpr int kRows = 256, kKeys = 128, kHalf = 64;
 constexpr int kPrefillThreads = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -321,7 +321,7 @@ __device__ __forceinline__ uint4 expand_values(uint32_t w)
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t scales[kScaleSlots];
-    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t s_full[2][2], p_full[2][2], o_done[2], o_final[2];  // [row tile][half tile]
     uint64_t packed_full[2][2], packed_empty[2][2];  // [keys, values][stage]
 };
 
@@ -356,24 +356,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kvh = blockIdx.y, split = blockIdx.z;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.bar.k_full[i], 128);
-            mbar_init(&sh.bar.k_empty[i], 1);
-            mbar_init(&sh.bar.v_full[i], 128);
-            mbar_init(&sh.bar.v_empty[i], 1);
-            mbar_init(&sh.bar.s_full[i], 1);
-            mbar_init(&sh.bar.p_full[i], 128);
-            mbar_init(&sh.bar.o_done[i], 1);
-            for (int w = 0; w < 2; ++w) {
-                mbar_init(&sh.bar.packed_full[w][i], 1);
-                mbar_init(&sh.bar.packed_empty[w][i], 4);
-            }
-        }
-        for (int i = 0; i < kScaleSlots; ++i)
-            mbar_init(&sh.bar.scales[i], 128);
-        fence_mbar_init();
-    }
     pdl_wait();
     pdl_launch_dependents();
     const Unit u = find_unit(p, blockIdx.x, sh.scratch());
@@ -385,6 +367,27 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     const int nq = rows > 128 ? 2 : 1;  // row tiles at work
 
     if (n > 0) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&sh.bar.k_full[i], 128);
+                mbar_init(&sh.bar.k_empty[i], nq);
+                mbar_init(&sh.bar.v_full[i], 128);
+                mbar_init(&sh.bar.v_empty[i], nq);
+                for (int h = 0; h < 2; ++h) {
+                    mbar_init(&sh.bar.s_full[i][h], 1);
+                    mbar_init(&sh.bar.p_full[i][h], 128);
+                }
+                mbar_init(&sh.bar.o_done[i], 1);
+                mbar_init(&sh.bar.o_final[i], 1);
+                for (int w = 0; w < 2; ++w) {
+                    mbar_init(&sh.bar.packed_full[w][i], 1);
+                    mbar_init(&sh.bar.packed_empty[w][i], 4);
+                }
+            }
+            for (int i = 0; i < kScaleSlots; ++i)
+                mbar_init(&sh.bar.scales[i], 128);
+            fence_mbar_init();
+        }
         if (warp == 12)
             tmem_alloc(&sh.tmem, 512);
         // Queries: 16-byte chunks of 8 values, rows of a block 128 bytes apart,
@@ -435,7 +438,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     }
 
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         // ---------------------------------------------------------- softmax
         const int s = warp >> 2;
         const int row = s * 128 + (warp & 3) * 32 + lane;
@@ -452,32 +454,32 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         const uint32_t ts = tmem + lane_at + s * 128, to = tmem + lane_at + 256 + s * D;
         float m = -INFINITY, lsum = 0.0f;  // m: base 2, of scale x scores
         bool poisoned = false, fine = s < nq;
-        for (int j = 0; j < n && fine; ++j) {
-            const int slot = j % kScaleSlots, j0 = (tl.first + j) * kKeys;
-            fine = mbar_wait_warp(&sh.bar.scales[slot], (j / kScaleSlots) & 1, p.c.err) &&
-                   mbar_wait_warp(&sh.bar.s_full[s], j & 1, p.c.err);
+#pragma unroll 1
+        for (int i = 0; i < 2 * n && fine; ++i) {  // half tiles
+            const int slot = (i >> 1) % kScaleSlots, half = i & 1;
+            const int j0 = (tl.first + (i >> 1)) * kKeys + half * kHalf;
+            if (half == 0)
+                fine = mbar_wait_warp(&sh.bar.scales[slot], ((i >> 1) / kScaleSlots) & 1, p.c.err);
+            fine = fine && mbar_wait_warp(&sh.bar.s_full[s][half], (i >> 1) & 1, p.c.err);
             if (!fine)
                 break;
             tc_fence_after();
-            uint32_t t[128];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                tmem_ld32_async(ts + 32 * i, t + 32 * i);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                tmem_arrived(t + 32 * i);
+            uint32_t t[kHalf];
+            tmem_ld32_async(ts + half * kHalf, t);
+            tmem_ld32_async(ts + half * kHalf + 32, t + 32);
             float mul = row_mul * sh.unit[slot];
             if (mul < 1.17549435e-38f)  // (NaN stays) no zero, which masks would meet
                 mul = 1.17549435e-38f;
-            const uint4 sk4 = sh.skip[slot], po4 = sh.poison[slot];
-            const uint32_t skip[4] = {sk4.x, sk4.y, sk4.z, sk4.w};
-            const uint32_t poison[4] = {po4.x, po4.y, po4.z, po4.w};
-            const bool special = (sk4.x | sk4.y | sk4.z | sk4.w | po4.x | po4.y | po4.z | po4.w) != 0;
-            if (special || j0 + kKeys - 1 > pos_min || j0 < low_max) {
+            const uint2 skip = reinterpret_cast<const uint2 *>(&sh.skip[slot])[half];
+            const uint2 poison = reinterpret_cast<const uint2 *>(&sh.poison[slot])[half];
+            tmem_ld_wait();
+            tmem_arrived(t);
+            tmem_arrived(t + 32);
+            const bool special = (skip.x | skip.y | poison.x | poison.y) != 0;
+            if (special || j0 + kHalf - 1 > pos_min || j0 < low_max) {
                 const int hi = pos - j0, lo = low - j0;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
+                for (int w = 0; w < 2; ++w) {
                     // keys of these 32 that the row sees, a bit each
                     uint32_t see = hi >= 32 * w + 31 ? 0xFFFFFFFFu
                                    : hi < 32 * w     ? 0u
@@ -485,78 +487,80 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                     see &= lo <= 32 * w          ? 0xFFFFFFFFu
                            : lo > 32 * w + 31 ? 0u
                                               : 0xFFFFFFFFu << (lo - 32 * w);
-                    see &= ~skip[w];
-                    poisoned = poisoned || (see & poison[w]);
+                    see &= ~(w ? skip.y : skip.x);
+                    poisoned = poisoned || (see & (w ? poison.y : poison.x));
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        t[32 * w + i] = (see >> i) & 1 ? t[32 * w + i] : 0xFF800000u;
+                    for (int k = 0; k < 32; ++k)
+                        t[32 * w + k] = (see >> k) & 1 ? t[32 * w + k] : 0xFF800000u;
                 }
             }
             float top[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                top[i] = fmaxf(__uint_as_float(t[32 * i]), __uint_as_float(t[32 * i + 1]));
+            for (int c = 0; c < 4; ++c) {
+                top[c] = fmaxf(__uint_as_float(t[16 * c]), __uint_as_float(t[16 * c + 1]));
 #pragma unroll
-                for (int k = 2; k < 32; k += 2)
-                    top[i] = fmaxf(top[i], fmaxf(__uint_as_float(t[32 * i + k]),
-                                                 __uint_as_float(t[32 * i + k + 1])));
+                for (int k = 2; k < 16; k += 2)
+                    top[c] = fmaxf(top[c], fmaxf(__uint_as_float(t[16 * c + k]),
+                                                 __uint_as_float(t[16 * c + k + 1])));
             }
             const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mul;
-            if (m == -INFINITY) {
+            if (m == -INFINITY)
                 m = mt;  // nothing summed up yet
-            }
             const bool grew = mt - m > 8.0f;
             if (__any_sync(0xffffffffu, grew)) {
                 const float a = grew ? ex2(m - mt) : 1.0f;
                 if (grew)
                     m = mt;
                 lsum *= a;
-                if (j > 0) {
-                    fine = mbar_wait_warp(&sh.bar.o_done[s], (j - 1) & 1, p.c.err);
+                if (i > 0) {
+                    // (the scores of i came after product i - 2: at most one
+                    // phase is out, and its parity is enough)
+                    fine = mbar_wait_warp(&sh.bar.o_done[s], (i - 1) & 1, p.c.err);
                     if (!fine)
                         break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int i = 0; i < D / 32; ++i) {
+                    for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
-                        tmem_ld32_async(to + 32 * i, o);
+                        tmem_ld32_async(to + 32 * c, o);
                         tmem_ld_wait();
                         tmem_arrived(o);
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                        tmem_st32_async(to + 32 * i, o);
+                        tmem_st32_async(to + 32 * c, o);
                     }
                     tmem_st_wait();
                 }
             }
             const float neg = m == -INFINITY ? 0.0f : -m;
-            const float2 *vs = reinterpret_cast<const float2 *>(sh.vs[slot]);
+            const float4 *vs = reinterpret_cast<const float4 *>(sh.vs[slot] + half * kHalf);
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            uint32_t pk[32];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t pk[32];
+            for (int k = 0; k < 16; ++k) {
+                const float4 v = vs[k];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int k = half * 64 + 2 * i;
-                    float2 x = fma2(make_float2(__uint_as_float(t[k]), __uint_as_float(t[k + 1])),
+                for (int c = 0; c < 2; ++c) {
+                    float2 x = fma2(make_float2(__uint_as_float(t[4 * k + 2 * c]),
+                                                __uint_as_float(t[4 * k + 2 * c + 1])),
                                     make_float2(mul, mul), make_float2(neg, neg));
                     x.x = ex2(x.x);
                     x.y = ex2(x.y);
-                    sum[i & 1] = add2(sum[i & 1], x);
-                    x = mul2(x, vs[half * 32 + i]);
-                    pk[i] = pack_bf16(x.x, x.y);
+                    sum[c] = add2(sum[c], x);
+                    x = mul2(x, c ? make_float2(v.z, v.w) : make_float2(v.x, v.y));
+                    pk[2 * k + c] = pack_bf16(x.x, x.y);
                 }
-                tmem_st32_async(ts + 32 * half, pk);
             }
+            tmem_st32_async(ts + half * kHalf, pk);
             lsum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&sh.bar.p_full[s]);
+            mbar_arrive(&sh.bar.p_full[s][half]);
         }
         // Output rows (a row tile without keys, or without rows, has none).
         if (n > 0 && s < nq) {
-            fine = fine && mbar_wait_warp(&sh.bar.o_done[s], (n - 1) & 1, p.c.err);
+            fine = fine && mbar_wait_warp(&sh.bar.o_final[s], 0, p.c.err);
             tc_fence_after();
         }
         const float inv = lsum == 0.0f ? 0.0f : poisoned ? NAN : 1.0f / lsum;
@@ -618,7 +622,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         }
         tc_fence_before();
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         // ------------------------------------------------- codes to operands
         // Thread i takes 16 bytes of codes of every kRowsAtOnce-th key. Lane l
         // of each warp looks after the scales of keys l, l + 32, ...
@@ -715,74 +718,83 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                 mbar_arrive(&sh.bar.packed_empty[1][st]);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         // -------------------------------------------------------------- MMAs
-        // The whole warp walks the loop, so that addresses and descriptors stay
-        // in uniform registers; one elected lane issues (issue by a lone lane of
-        // a divergent branch took 100 cycles a product, twice its execution).
-        if (warp == 12 && n > 0) {
-            constexpr uint32_t kQk = idesc_f16(128, 128, false, false);
+        // One warp per row tile: a product is queued only a few deep, so what
+        // one warp spends on waits and commits the other's products cover. The
+        // whole warp walks the loop, so that addresses and descriptors stay in
+        // uniform registers; one elected lane issues (issue by a lone lane of a
+        // divergent branch took 100 cycles a product, twice its execution).
+        const int s = (warp - 12) >> 1;
+        if ((warp & 1) == 0 && s < nq && n > 0) {
+            constexpr uint32_t kQk = idesc_f16(128, kHalf, false, false);
             constexpr uint32_t kPv = idesc_f16(128, D, true, true);
-            const uint64_t q0 = umma_desc_sw128(smem_u32(sh.q)), k0 = umma_desc_sw128(smem_u32(sh.k));
+            const uint64_t q0 = umma_desc_sw128(smem_u32(sh.q[s]));
+            const uint64_t k0 = umma_desc_sw128(smem_u32(sh.k));
             const uint64_t v0 = umma_desc_mn_sw128(smem_u32(sh.v), 16384);
+            const uint32_t s_at = tmem + s * 128, o_at = tmem + 256 + s * D;
             const bool lead = elect_one();
-            auto scores = [&](int s, int st) {
-                const uint64_t a = umma_desc_advance(q0, s * S::kTileBytes);
-                const uint64_t b = umma_desc_advance(k0, st * S::kTileBytes);
+            // Scores of a half tile of 64 keys of the stage, and the products
+            // with its values. Scores run two half tiles ahead: the softmax
+            // finds them ready. A half tile's weights lie in its scores'
+            // columns, which the scores after next may overwrite as one
+            // thread's products execute in order.
+            auto scores = [&](int stage, int half) {
+                const uint64_t b = umma_desc_advance(k0, stage * S::kTileBytes + half * kHalf * 128);
                 if (lead) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t at = (k >> 2) * 16384 + (k & 3) * 32;
-                        umma_f16(tmem + s * 128, umma_desc_advance(a, at), umma_desc_advance(b, at),
-                                 kQk, k > 0);
+                        umma_f16(s_at + half * kHalf, umma_desc_advance(q0, at),
+                                 umma_desc_advance(b, at), kQk, k > 0);
                     }
-                    umma_commit(&sh.bar.s_full[s]);
+                    umma_commit(&sh.bar.s_full[s][half]);
                 }
             };
-            auto values = [&](int s, int st, bool first) {
-                const uint64_t b = umma_desc_advance(v0, st * S::kTileBytes);
+            auto values = [&](int stage, int half, bool first, bool final) {
+                const uint64_t b = umma_desc_advance(v0, stage * S::kTileBytes + half * kHalf * 128);
                 if (lead) {
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        umma_f16_ts(tmem + 256 + s * D, tmem + s * 128 + k * 8,
-                                    umma_desc_advance(b, k * 2048), kPv, !first || k > 0);
-                    umma_commit(&sh.bar.o_done[s]);
+                    for (int k = 0; k < kHalf / 16; ++k)
+                        umma_f16_ts(o_at, s_at + half * kHalf + k * 8, umma_desc_advance(b, k * 2048),
+                                    kPv, !first || k > 0);
+                    umma_commit(final ? &sh.bar.o_final[s] : &sh.bar.o_done[s]);
                 }
             };
             bool fine = mbar_wait_warp(&sh.bar.k_full[0], 0, p.c.err);
             if (fine) {
                 tc_fence_after();
-                for (int s = 0; s < nq; ++s)
-                    scores(s, 0);
-                if (n > 2 && lead)
+                scores(0, 0);
+                scores(0, 1);
+                if (n > 2 && lead)  // (no arrival that nobody waits for)
                     umma_commit(&sh.bar.k_empty[0]);
             }
 #pragma unroll 1
             for (int j = 0; j < n && fine; ++j) {
-                const int st = j & 1, parity = (j >> 1) & 1, nst = (j + 1) & 1;
-                fine = mbar_wait_warp(&sh.bar.v_full[st], parity, p.c.err);
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (s >= nq || !fine)
-                        break;
-                    fine = mbar_wait_warp(&sh.bar.p_full[s], j & 1, p.c.err);
+                const int st = j & 1;
+                fine = mbar_wait_warp(&sh.bar.v_full[st], (j >> 1) & 1, p.c.err) &&
+                       mbar_wait_warp(&sh.bar.p_full[s][0], j & 1, p.c.err);
+                if (!fine)
+                    break;
+                tc_fence_after();
+                values(st, 0, j == 0, false);
+                if (j + 1 < n) {
+                    fine = mbar_wait_warp(&sh.bar.k_full[st ^ 1], ((j + 1) >> 1) & 1, p.c.err);
                     if (!fine)
                         break;
                     tc_fence_after();
-                    values(s, st, j == 0);
-                    if (s == nq - 1 && j + 2 < n && lead)  // (no arrival after the last wait)
-                        umma_commit(&sh.bar.v_empty[st]);
-                    if (j + 1 < n) {
-                        if (s == 0) {
-                            fine = mbar_wait_warp(&sh.bar.k_full[nst], ((j + 1) >> 1) & 1, p.c.err);
-                            if (!fine)
-                                break;
-                            tc_fence_after();
-                        }
-                        scores(s, nst);
-                        if (s == nq - 1 && j + 3 < n && lead)
-                            umma_commit(&sh.bar.k_empty[nst]);
-                    }
+                    scores(st ^ 1, 0);
+                }
+                fine = mbar_wait_warp(&sh.bar.p_full[s][1], j & 1, p.c.err);
+                if (!fine)
+                    break;
+                tc_fence_after();
+                values(st, 1, false, j == n - 1);
+                if (j + 2 < n && lead)
+                    umma_commit(&sh.bar.v_empty[st]);
+                if (j + 1 < n) {
+                    scores(st ^ 1, 1);
+                    if (j + 3 < n && lead)
+                        umma_commit(&sh.bar.k_empty[st ^ 1]);
                 }
             }
         }
