@@ -59,7 +59,8 @@ struct PrefillParams {
     Kv4Query q;
     const int32_t *tok_start, *lens;
     int T, rep, splits;
-    float *parts;  // [units][kv_heads][splits][256][D + 2] where splits > 1
+    float *parts;   // [units][kv_heads][splits][256][D] where splits > 1
+    float2 *sums;   // [units][kv_heads][splits][256]: maximum (base 2), sum
 };
 
 // Unit (256 rows) `unit` of the call: its sequence, and where its rows begin.
@@ -273,6 +274,13 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// Of a query row whose largest magnitude has these fp32 bits: the power of two
+// that its fp16 values are taken against.
+__device__ __forceinline__ int row_exponent(uint32_t top)
+{
+    return min(max(int(top >> 23) - 127, -100), 126);
+}
+
 template <class T2>
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b)
 {
@@ -321,6 +329,7 @@ __device__ __forceinline__ uint4 expand_values(uint32_t w)
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t scales[kScaleSlots];
+    uint64_t q_full[2];
     uint64_t s_full[2][2], p_full[2][2], o_done[2], o_final[2];  // [row tile][half tile]
     uint64_t packed_full[2][2], packed_empty[2][2];  // [keys, values][stage]
 };
@@ -341,9 +350,10 @@ struct Shared {
     uint32_t pages[2];          // [stage] pages that are there, and << 16 bad ones
     uint32_t tmem;
     Bars bar;
-    // only until the roles part:
-    __device__ __forceinline__ float *row_unit() { return reinterpret_cast<float *>(v[1]); }
-    __device__ __forceinline__ int *scratch() { return reinterpret_cast<int *>(v[0]); }
+    __device__ __forceinline__ int *scratch()  // only until the roles part
+    {
+        return reinterpret_cast<int *>(v[0]);
+    }
 };
 
 template <int D>
@@ -379,6 +389,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                 }
                 mbar_init(&sh.bar.o_done[i], 1);
                 mbar_init(&sh.bar.o_final[i], 1);
+                mbar_init(&sh.bar.q_full[i], 128);
                 for (int w = 0; w < 2; ++w) {
                     mbar_init(&sh.bar.packed_full[w][i], 1);
                     mbar_init(&sh.bar.packed_empty[w][i], 4);
@@ -390,52 +401,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         }
         if (warp == 12)
             tmem_alloc(&sh.tmem, 512);
-        // Queries: 16-byte chunks of 8 values, rows of a block 128 bytes apart,
-        // D / 8 neighbouring lanes a row.
-        for (int i = threadIdx.x; i < kRows * (D / 8); i += kPrefillThreads) {
-            const int r = i / (D / 8), ch = i - r * (D / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < rows) {
-                const int tok = (u.row0 + r) / p.rep, h = (u.row0 + r) - tok * p.rep;
-                v = __ldg(reinterpret_cast<const uint4 *>(
-                    p.q.q + (u.start + tok) * p.q.q_stride +
-                    (long long)(kvh * p.rep + h) * D + ch * 8));
-            }
-            const float f[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
-                                bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
-            uint32_t top = 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                top = max(top, __float_as_uint(f[k]) & 0x7FFFFFFFu);
-#pragma unroll
-            for (int o = D / 16; o > 0; o >>= 1)
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int k = max(int(top >> 23) - 127, -100);
-            const float down = __uint_as_float(uint32_t(127 - min(k, 126)) << 23);
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __half2 x = __floats2half2_rn(f[e] * down, f[4 + e] * down);
-                w[e] = *reinterpret_cast<const uint32_t *>(&x);
-            }
-            *reinterpret_cast<uint4 *>(sh.q[r >> 7] + (ch >> 3) * 16384 +
-                                       sw128_off(r & 127, ch & 7)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-            if (ch == 0)
-                sh.row_unit()[r] = top >= 0x7F800000u ? NAN : 1.0f / down;
-        }
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
     }
     const uint32_t tmem = n > 0 ? sh.tmem : 0;
-    float row_mul = 0.0f;
-    if (n > 0) {
-        if (warp < 8)
-            row_mul = sh.row_unit()[threadIdx.x] * (p.q.scale * kLog2e);
-        __syncthreads();
-    }
 
     if (warp < 8) {
         // ---------------------------------------------------------- softmax
@@ -452,6 +422,57 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             p.q.window > 0 ? u.pos0 + (u.row0 + last) / p.rep - p.q.window + 1 : 0;
         const uint32_t lane_at = uint32_t((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_at + s * 128, to = tmem + lane_at + 256 + s * D;
+        const long long row_at = (long long)(kvh * p.rep + h) * D;  // within its token's row
+        // The warp's query rows, D/8 lanes a row, all loads at once (while the
+        // first keys are fetched and expanded), then fp16 against each row's
+        // largest magnitude.
+        float row_mul = 0.0f;  // what 1 in the row stands for x scale, base 2
+        if (n > 0 && s < nq) {
+            constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks, kTimes = kChunks;
+            const int c = lane % kChunks;
+            const unsigned long long src = reinterpret_cast<unsigned long long>(
+                real ? p.q.q + (u.start + tok) * p.q.q_stride + row_at : nullptr);
+            uint4 v[kTimes];
+#pragma unroll
+            for (int i = 0; i < kTimes; ++i) {
+                const uint4 *from = reinterpret_cast<const uint4 *>(
+                    __shfl_sync(0xffffffffu, src, i * kAtOnce + lane / kChunks));
+                v[i] = from ? __ldg(from + c) : make_uint4(0, 0, 0, 0);
+            }
+            uint32_t mine = 0;  // largest magnitude of the thread's own row, fp32 bits
+#pragma unroll
+            for (int i = 0; i < kTimes; ++i) {
+                uint32_t top = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                        __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+                top = max(top & 0xFFFFu, top >> 16) << 16;
+#pragma unroll
+                for (int o = kChunks / 2; o > 0; o >>= 1)
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const uint32_t its = __shfl_sync(0xffffffffu, top, (lane % kAtOnce) * kChunks);
+                if (lane / kAtOnce == i)
+                    mine = its;
+                const float down = __uint_as_float(uint32_t(127 - row_exponent(top)) << 23);
+                const float f[8] = {bf16_lo(v[i].x), bf16_hi(v[i].x), bf16_lo(v[i].y),
+                                    bf16_hi(v[i].y), bf16_lo(v[i].z), bf16_hi(v[i].z),
+                                    bf16_lo(v[i].w), bf16_hi(v[i].w)};
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __half2 x = __floats2half2_rn(f[e] * down, f[4 + e] * down);
+                    w[e] = *reinterpret_cast<const uint32_t *>(&x);
+                }
+                *reinterpret_cast<uint4 *>(
+                    sh.q[s] + (c >> 3) * 16384 +
+                    sw128_off((warp & 3) * 32 + i * kAtOnce + lane / kChunks, c & 7)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            row_mul = mine >= 0x7F800000u
+                          ? NAN
+                          : __uint_as_float(uint32_t(127 + row_exponent(mine)) << 23) *
+                                (p.q.scale * kLog2e);
+            fence_proxy_async_smem();
+            mbar_arrive(&sh.bar.q_full[s]);
+        }
         float m = -INFINITY, lsum = 0.0f;  // m: base 2, of scale x scores
         bool poisoned = false, fine = s < nq;
 #pragma unroll 1
@@ -565,12 +586,35 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         }
         const float inv = lsum == 0.0f ? 0.0f : poisoned ? NAN : 1.0f / lsum;
         const long long token = u.start + tok;
-        const int head = kvh * p.rep + h;
-        float *part = p.splits == 1
-                          ? nullptr
-                          : p.parts + ((((long long)blockIdx.x * p.c.kv_heads + kvh) * p.splits +
-                                        split) * kRows + row) * (D + 2);
+        const long long part = ((((long long)blockIdx.x * p.c.kv_heads + kvh) * p.splits + split) *
+                                kRows + row);
         if (s < nq) {
+            // Rows change lanes in shared memory (the row tile's queries are done
+            // with), so that D/8 lanes store the 2 D bytes of one row: results in
+            // bf16, or fp32 parts D/2 values at a time.
+            constexpr int kChunks = D / 8;  // of 16 bytes
+            uint8_t *stage = sh.q[s] + (warp & 3) * 32 * (2 * D);
+            const bool parts = p.splits > 1;
+            char *dst = parts ? reinterpret_cast<char *>(p.parts + part * D)
+                              : reinterpret_cast<char *>(p.q.out + token * p.q.out_stride + row_at);
+            if (!real)
+                dst = nullptr;
+            auto put = [&](int chunk, uint4 v) {
+                *reinterpret_cast<uint4 *>(stage + lane * 2 * D + ((chunk ^ (lane & 7)) << 4)) = v;
+            };
+            auto flush = [&](int offset) {
+                __syncwarp();
+#pragma unroll 4
+                for (int r0 = 0; r0 < 32; r0 += 32 / kChunks) {
+                    const int r = r0 + lane / kChunks, c = lane % kChunks;
+                    const uint4 v = lds128(stage + r * 2 * D + ((c ^ (r & 7)) << 4));
+                    char *to_row = reinterpret_cast<char *>(__shfl_sync(
+                        0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
+                    if (to_row)
+                        *reinterpret_cast<uint4 *>(to_row + offset + c * 16) = v;
+                }
+                __syncwarp();
+            };
 #pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
                 uint32_t o[32];
@@ -583,8 +627,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                     for (int k = 0; k < 32; ++k)
                         o[k] = 0;
                 }
-                if (!real)
-                    continue;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     float e[8];  // back from the order 0 4 1 5 2 6 3 7
@@ -593,31 +635,30 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                         e[k] = __uint_as_float(o[8 * c + 2 * k]);
                         e[4 + k] = __uint_as_float(o[8 * c + 2 * k + 1]);
                     }
-                    if (part) {
+                    const float by = parts ? poisoned ? NAN : 1.0f : inv;
 #pragma unroll
-                        for (int k = 0; k < 8; k += 2)
-                            *reinterpret_cast<float2 *>(part + 32 * i + 8 * c + k) =
-                                poisoned ? make_float2(NAN, NAN)
-                                         : lsum == 0.0f ? make_float2(0.0f, 0.0f)
-                                                        : make_float2(e[k], e[k + 1]);
+                    for (int k = 0; k < 8; ++k)
+                        e[k] = lsum == 0.0f ? 0.0f : e[k] * by;
+                    if (parts) {
+                        const int at = (32 * i) % (D / 2) / 4 + 2 * c;
+                        put(at, make_uint4(__float_as_uint(e[0]), __float_as_uint(e[1]),
+                                           __float_as_uint(e[2]), __float_as_uint(e[3])));
+                        put(at + 1, make_uint4(__float_as_uint(e[4]), __float_as_uint(e[5]),
+                                               __float_as_uint(e[6]), __float_as_uint(e[7])));
                     } else {
-                        uint4 v;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            e[k] = lsum == 0.0f ? 0.0f : e[k] * inv;
-                        v.x = pack_bf16(e[0], e[1]);
-                        v.y = pack_bf16(e[2], e[3]);
-                        v.z = pack_bf16(e[4], e[5]);
-                        v.w = pack_bf16(e[6], e[7]);
-                        *reinterpret_cast<uint4 *>(p.q.out + token * p.q.out_stride +
-                                                   (long long)head * D + 32 * i + 8 * c) = v;
+                        put(4 * i + c, make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]),
+                                                  pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7])));
                     }
                 }
+                if (parts && 32 * (i + 1) % (D / 2) == 0)
+                    flush(32 * i / (D / 2) * 2 * D);
             }
-            if (real && part)
-                *reinterpret_cast<float2 *>(part + D) = make_float2(m, lsum);
+            if (!parts)
+                flush(0);
+            if (real && parts)
+                p.sums[part] = make_float2(m, lsum);
             else if (real && p.q.lse)
-                p.q.lse[token * p.q.q_heads + head] =
+                p.q.lse[token * p.q.q_heads + kvh * p.rep + h] =
                     lsum == 0.0f ? -INFINITY : (m + __log2f(lsum)) * kLn2;
         }
         tc_fence_before();
@@ -760,7 +801,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                     umma_commit(final ? &sh.bar.o_final[s] : &sh.bar.o_done[s]);
                 }
             };
-            bool fine = mbar_wait_warp(&sh.bar.k_full[0], 0, p.c.err);
+            bool fine = mbar_wait_warp(&sh.bar.q_full[s], 0, p.c.err) &&
+                        mbar_wait_warp(&sh.bar.k_full[0], 0, p.c.err);
             if (fine) {
                 tc_fence_after();
                 scores(0, 0);
@@ -883,15 +925,14 @@ __global__ void __launch_bounds__(kJoinThreads)
         return;
     const int kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = min(kRows, u.n * p.rep - u.row0);
-    const float *unit = p.parts +
-                        ((long long)blockIdx.x * p.c.kv_heads + kvh) * p.splits * kRows * (D + 2);
+    const long long unit = ((long long)blockIdx.x * p.c.kv_heads + kvh) * p.splits * kRows;
     for (int r = blockIdx.z * kJoinRows + warp; r < min(rows, int(blockIdx.z + 1) * kJoinRows);
          r += kJoinThreads / 32) {
-        auto part = [&](int k) { return unit + ((long long)k * kRows + r) * (D + 2); };
+        auto part = [&](int k) { return unit + (long long)k * kRows + r; };
         // lane k: part k's maximum and sum
         float2 ml = make_float2(-INFINITY, 0.0f);
         if (lane < p.splits)
-            ml = *reinterpret_cast<const float2 *>(part(lane) + D);
+            ml = p.sums[part(lane)];
         float m = ml.x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -906,7 +947,7 @@ __global__ void __launch_bounds__(kJoinThreads)
             const float wk = __shfl_sync(0xffffffffu, w, k);
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
-                const float2 x = *reinterpret_cast<const float2 *>(part(k) + i * 64 + 2 * lane);
+                const float2 x = *reinterpret_cast<const float2 *>(p.parts + part(k) * D + i * 64 + 2 * lane);
                 v[i].x = fmaf(wk, x.x, v[i].x);
                 v[i].y = fmaf(wk, x.y, v[i].y);
             }
@@ -957,8 +998,8 @@ PrefillPlan plan_prefill(const Kv4View &c, int D, int q_heads, int T)
         }
     }
     d.bytes = d.splits == 1 ? 0
-                            : size_t(d.units) * c.kv_heads * d.splits * kRows * size_t(D + 2) *
-                                  sizeof(float);
+                            : size_t(d.units) * c.kv_heads * d.splits * kRows *
+                                  (size_t(D) * sizeof(float) + sizeof(float2));
     return d;
 }
 
@@ -1019,6 +1060,8 @@ cudaError_t launch_kv4_prefill(const Kv4View &c, int D, const Kv4Query &q,
     p.rep = plan.rep;
     p.splits = plan.splits;
     p.parts = static_cast<float *>(workspace);
+    p.sums = reinterpret_cast<float2 *>(p.parts + size_t(plan.units) * c.kv_heads * plan.splits *
+                                                      kRows * size_t(D));
     return D == 128 ? launch<128>(p, plan, stream) : launch<64>(p, plan, stream);
 }
 
