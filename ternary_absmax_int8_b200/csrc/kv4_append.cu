@@ -29,18 +29,43 @@ struct AppendParams {
     int T;
 };
 
-// The whole number nearest to x / s, ties to even, for |x / s| < 2^23. The
-// rounded quotient can sit on a half where x / s does not; the sign of the
-// exact remainder x - t s (exact: t has 5 bits, s 8) decides then.
-__device__ __forceinline__ int kv4_code(float x, float s)
+// Eight codes + 8, four bits each, first value lowest: the whole numbers
+// nearest to x / s, ties to even. x times the rounded 1 / s is off by less than
+// 2^-20, so its nearest whole number q is the right one or its neighbour, and
+// the exact remainder x - q s (24 bits hold it: q s has 11, and it is smaller
+// than x or than s) tells: beyond s / 2, or at it with q odd, the code is the
+// neighbour on x's side. Adding 1.5 2^23 rounds to a whole number and leaves it
+// in the low bits, where the sum of 16^i times those bits packs the codes. (A
+// correctly rounded quotient and its checks took 40 instructions a value and
+// bound prompts by arithmetic at 29 us; this takes 8.)
+__device__ __forceinline__ uint32_t pack_codes(const float (&x)[8], float s)
 {
-    const float t = __fdiv_rn(x, s);
-    float q = rintf(t);
-    if (fabsf(t - truncf(t)) == 0.5f) {
-        const float rest = __fmaf_rn(-t, s, x);
-        q = rest > 0.0f ? ceilf(t) : rest < 0.0f ? floorf(t) : q;
+    constexpr float kMagic = 12582912.0f;
+    constexpr uint32_t kOnes = 0x11111111u;
+    // a scale below 2^-100 is lifted: its reciprocal could overflow
+    const float lift = s < 7.9e-31f ? 1.2676506e30f : 1.0f;  // 2^100
+    const float sl = s * lift, inv = __frcp_rn(sl);
+    float t[8], far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float xl = x[i] * lift;
+        t[i] = __fmaf_rn(xl, inv, kMagic);
+        far = fmaxf(far, fabsf(__fmaf_rn(kMagic - t[i], sl, xl)));
     }
-    return int(q);
+    if (2.0f * far >= sl) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float e = __fmaf_rn(kMagic - t[i], sl, x[i] * lift), h = 2.0f * fabsf(e);
+            if (h > sl || (h == sl && (__float_as_uint(t[i]) & 1u)))
+                t[i] += e > 0.0f ? 1.0f : -1.0f;
+        }
+    }
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        w += __float_as_uint(t[i]) << (4 * i);
+    // less the magic number's own bits, plus 8 in each place
+    return w - 0x4B400000u * kOnes + 8u * kOnes;
 }
 
 template <bool F32>
@@ -76,13 +101,8 @@ __device__ __forceinline__ void put_row(const float (&x)[8], int lane, uint8_t *
     uint16_t sbits = 0x7FC0;        // NaN: the row holds a NaN or an infinity
     if (m < 0x7F800000u) {
         sbits = bf16_bits(__fdiv_rn(__uint_as_float(m), 7.0f));
-        if (sbits != 0) {
-            const float s = __uint_as_float(uint32_t(sbits) << 16);
-            packed = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                packed |= uint32_t(kv4_code(x[i], s) + 8) << (4 * i);
-        }
+        if (sbits != 0)
+            packed = pack_codes(x, __uint_as_float(uint32_t(sbits) << 16));
     }
     if (store) {
         *reinterpret_cast<uint32_t *>(codes + 4 * lane) = packed;

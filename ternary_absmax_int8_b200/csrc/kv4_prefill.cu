@@ -235,6 +235,15 @@ __device__ __forceinline__ void tmem_arrived(uint32_t *v)
                  "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]));
 }
 
+// One arrival for the warp, after all of its lanes' work (32 arrivals on one
+// barrier go through shared memory one by one).
+__device__ __forceinline__ void warp_arrive(uint64_t *bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(bar);
+}
+
 // Pairs of fp32 values in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
@@ -379,24 +388,24 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     if (n > 0) {
         if (threadIdx.x == 0) {
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&sh.bar.k_full[i], 128);
+                mbar_init(&sh.bar.k_full[i], 4);
                 mbar_init(&sh.bar.k_empty[i], nq);
-                mbar_init(&sh.bar.v_full[i], 128);
+                mbar_init(&sh.bar.v_full[i], 4);
                 mbar_init(&sh.bar.v_empty[i], nq);
                 for (int h = 0; h < 2; ++h) {
                     mbar_init(&sh.bar.s_full[i][h], 1);
-                    mbar_init(&sh.bar.p_full[i][h], 128);
+                    mbar_init(&sh.bar.p_full[i][h], 4);
                 }
                 mbar_init(&sh.bar.o_done[i], 1);
                 mbar_init(&sh.bar.o_final[i], 1);
-                mbar_init(&sh.bar.q_full[i], 128);
+                mbar_init(&sh.bar.q_full[i], 4);
                 for (int w = 0; w < 2; ++w) {
                     mbar_init(&sh.bar.packed_full[w][i], 1);
                     mbar_init(&sh.bar.packed_empty[w][i], 4);
                 }
             }
             for (int i = 0; i < kScaleSlots; ++i)
-                mbar_init(&sh.bar.scales[i], 128);
+                mbar_init(&sh.bar.scales[i], 4);
             fence_mbar_init();
         }
         if (warp == 12)
@@ -471,7 +480,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                           : __uint_as_float(uint32_t(127 + row_exponent(mine)) << 23) *
                                 (p.q.scale * kLog2e);
             fence_proxy_async_smem();
-            mbar_arrive(&sh.bar.q_full[s]);
+            warp_arrive(&sh.bar.q_full[s]);
         }
         float m = -INFINITY, lsum = 0.0f;  // m: base 2, of scale x scores
         bool poisoned = false, fine = s < nq;
@@ -577,7 +586,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             lsum += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&sh.bar.p_full[s][half]);
+            warp_arrive(&sh.bar.p_full[s][half]);
         }
         // Output rows (a row tile without keys, or without rows, has none).
         if (n > 0 && s < nq) {
@@ -740,11 +749,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             }
             if (i == 0)
                 sh.unit[slot] = __uint_as_float((top - 11u) << 23);
-            mbar_arrive(&sh.bar.scales[slot]);
+            warp_arrive(&sh.bar.scales[slot]);
             expand(sh.k[st], sh.packed[0][st], true, scale);
             fence_proxy_async_smem();
-            mbar_arrive(&sh.bar.k_full[st]);
-            __syncwarp();
+            warp_arrive(&sh.bar.k_full[st]);
             if (lane == 0)
                 mbar_arrive(&sh.bar.packed_empty[0][st]);
             fine = (j < 2 || mbar_wait_warp(&sh.bar.v_empty[st], parity ^ 1, p.c.err)) &&
@@ -753,8 +761,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                 break;
             expand(sh.v[st], sh.packed[1][st], false, scale);
             fence_proxy_async_smem();
-            mbar_arrive(&sh.bar.v_full[st]);
-            __syncwarp();
+            warp_arrive(&sh.bar.v_full[st]);
             if (lane == 0)
                 mbar_arrive(&sh.bar.packed_empty[1][st]);
         }
