@@ -24,39 +24,37 @@ constexpr int kAppendThreads = 256;
 struct AppendParams {
     Kv4View c;
     const void *k, *v;  // rows [T, kv_heads, D], bf16 or fp32
-    long long k_stride, v_stride;
+    // strides and counts fit 32 bits, so that an address is one multiply-add
+    unsigned k_stride, v_stride, page_stride;
     const int32_t *tok_start, *lens;
-    int T;
+    int T, items;  // items: (token, head) pairs
+    int per_cta;   // of them, a multiple of the CTA's groups
 };
 
 // Eight codes + 8, four bits each, first value lowest: the whole numbers
-// nearest to x / s, ties to even. x times the rounded 1 / s is off by less than
-// 2^-20, so its nearest whole number q is the right one or its neighbour, and
-// the exact remainder x - q s (24 bits hold it: q s has 11, and it is smaller
-// than x or than s) tells: beyond s / 2, or at it with q odd, the code is the
-// neighbour on x's side. Adding 1.5 2^23 rounds to a whole number and leaves it
-// in the low bits, where the sum of 16^i times those bits packs the codes. (A
-// correctly rounded quotient and its checks took 40 instructions a value and
-// bound prompts by arithmetic at 29 us; this takes 8.)
-__device__ __forceinline__ uint32_t pack_codes(const float (&x)[8], float s)
+// nearest to x / s, ties to even; inv is 1 / s to 2^-22. x times inv is off by
+// less than 2^-18, so its nearest whole number q is the right one or its
+// neighbour, and the exact remainder x - q s (24 bits hold it: q s has 11, and
+// it is smaller than x or than s) tells: beyond s / 2, or at it with q odd, the
+// code is the neighbour on x's side. Adding 1.5 2^23 rounds to a whole number
+// and leaves it in the low bits, where the sum of 16^i times those bits packs
+// the codes. (A correctly rounded quotient and its checks took 40 instructions
+// a value and bound prompts by arithmetic.)
+__device__ __forceinline__ uint32_t pack_codes(const float (&x)[8], float s, float inv)
 {
     constexpr float kMagic = 12582912.0f;
     constexpr uint32_t kOnes = 0x11111111u;
-    // a scale below 2^-100 is lifted: its reciprocal could overflow
-    const float lift = s < 7.9e-31f ? 1.2676506e30f : 1.0f;  // 2^100
-    const float sl = s * lift, inv = __frcp_rn(sl);
     float t[8], far = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float xl = x[i] * lift;
-        t[i] = __fmaf_rn(xl, inv, kMagic);
-        far = fmaxf(far, fabsf(__fmaf_rn(kMagic - t[i], sl, xl)));
+        t[i] = __fmaf_rn(x[i], inv, kMagic);
+        far = fmaxf(far, fabsf(__fmaf_rn(kMagic - t[i], s, x[i])));
     }
-    if (2.0f * far >= sl) {
+    if (2.0f * far >= s) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float e = __fmaf_rn(kMagic - t[i], sl, x[i] * lift), h = 2.0f * fabsf(e);
-            if (h > sl || (h == sl && (__float_as_uint(t[i]) & 1u)))
+            const float e = __fmaf_rn(kMagic - t[i], s, x[i]), h = 2.0f * fabsf(e);
+            if (h > s || (h == s && (__float_as_uint(t[i]) & 1u)))
                 t[i] += e > 0.0f ? 1.0f : -1.0f;
         }
     }
@@ -66,6 +64,37 @@ __device__ __forceinline__ uint32_t pack_codes(const float (&x)[8], float s)
         w += __float_as_uint(t[i]) << (4 * i);
     // less the magic number's own bits, plus 8 in each place
     return w - 0x4B400000u * kOnes + 8u * kOnes;
+}
+
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The larger, NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Bits of the row's largest magnitude; as unsigned whole numbers they order with
+// infinity and NaN on top, so neither is dropped.
+template <int D>
+__device__ __forceinline__ uint32_t row_top(const float (&x)[8])
+{
+    float m = fabsf(x[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+        m = max_nan(m, fabsf(x[i]));
+    uint32_t top = __float_as_uint(m) & 0x7FFFFFFFu;
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return top;
 }
 
 template <bool F32>
@@ -83,88 +112,146 @@ __device__ __forceinline__ void load_row8(const void *base, long long at, float 
     }
 }
 
-// Quantise the group's row and store its codes (4 bytes a lane) and scale.
+// Store the group's row as codes (4 bytes a lane) and its scale's bits; inv is
+// the scale's reciprocal.
 template <int D>
-__device__ __forceinline__ void put_row(const float (&x)[8], int lane, uint8_t *codes,
-                                        uint16_t *scale, bool store)
+__device__ __forceinline__ void put_row(const float (&x)[8], uint32_t sbits, float inv, int lane,
+                                        uint8_t *codes, uint16_t *scale, bool store)
 {
-    // The largest magnitude; as unsigned whole numbers the bit patterns of
-    // magnitudes order with infinity and NaN on top, so neither is dropped.
-    uint32_t m = 0;
+    uint32_t packed = 0x88888888u;  // eight codes 0: a row of zeros, or one that holds a NaN
+    if (inv != 0.0f) {
+        float s = __uint_as_float(sbits << 16);
+        if (s < 7.9e-31f) {
+            // below 2^-100 all is lifted by 2^100, as 1 / s might be infinite
+            constexpr float kLift = 1.2676506002282294e30f;
+            float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = D / 16; o > 0; o >>= 1)
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    uint32_t packed = 0x88888888u;  // eight codes 0
-    uint16_t sbits = 0x7FC0;        // NaN: the row holds a NaN or an infinity
-    if (m < 0x7F800000u) {
-        sbits = bf16_bits(__fdiv_rn(__uint_as_float(m), 7.0f));
-        if (sbits != 0)
-            packed = pack_codes(x, __uint_as_float(uint32_t(sbits) << 16));
+            for (int i = 0; i < 8; ++i)
+                y[i] = x[i] * kLift;
+            packed = pack_codes(y, s * kLift, inv);
+        } else {
+            packed = pack_codes(x, s, inv);
+        }
     }
     if (store) {
         *reinterpret_cast<uint32_t *>(codes + 4 * lane) = packed;
         if (lane == 0)
-            *scale = sbits;
+            *scale = uint16_t(sbits);
     }
 }
 
 template <int D, bool F32>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 4)
     kv4_append_kernel(const __grid_constant__ AppendParams p)
 {
-    constexpr int kLanes = D / 8;
+    constexpr int kLanes = D / 8, kGroups = kAppendThreads / kLanes;
     const int lane = threadIdx.x % kLanes;
-    const long long item =
-        (long long)blockIdx.x * (kAppendThreads / kLanes) + threadIdx.x / kLanes;
     pdl_wait();
     pdl_launch_dependents();
-    // Lanes without a row stay for the shuffles and store nothing.
-    const bool real = item < (long long)p.T * p.c.kv_heads;
-    const int t = real ? int(item / p.c.kv_heads) : 0;
-    const int h = real ? int(item - (long long)t * p.c.kv_heads) : 0;
-    float k[8], v[8];
-    load_row8<F32>(p.k, t * p.k_stride + h * D + lane * 8, k);
-    load_row8<F32>(p.v, t * p.v_stride + h * D + lane * 8, v);
+    // A CTA's items are consecutive (token, head) pairs, kGroups at a time; the
+    // next ones' rows are on their way while the present ones are quantised.
+    const int start = blockIdx.x * p.per_cta, first = start + threadIdx.x / kLanes;
+    const int stop = min(p.items - start, p.per_cta) + start;
+    float k[8], v[8], next_k[8], next_v[8];
+    int t = first / p.c.kv_heads, h = first - t * p.c.kv_heads;
+    auto load = [&](bool real, int at, int head, float (&kk)[8], float (&vv)[8]) {
+        if (real) {
+            const unsigned in = head * D + lane * 8;
+            load_row8<F32>(p.k, (long long)((unsigned long long)unsigned(at) * p.k_stride + in), kk);
+            load_row8<F32>(p.v, (long long)((unsigned long long)unsigned(at) * p.v_stride + in), vv);
+        }
+    };
+    load(first < stop, t, h, k, v);
 
     // The token's sequence: the last b with tok_start[b] <= t.
-    bool store = real;
-    int b = t, behind = 1;  // tokens from t to its sequence's end
+    int b = t, seq_end = t + 1, begin = 0, end = p.T;
     if (p.tok_start) {
-        int lo = 0, hi = p.c.batch;  // tok_start[lo] <= t < tok_start[hi]
-        store = store && p.tok_start[0] <= t && t < p.tok_start[hi];
+        begin = p.tok_start[0];
+        end = p.tok_start[p.c.batch];
+        int lo = 0, hi = p.c.batch;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             (p.tok_start[mid] <= t ? lo : hi) = mid;
         }
         b = lo;
-        behind = p.tok_start[lo + 1] - t;
+        seq_end = p.tok_start[lo + 1];
     }
-    uint8_t *codes = nullptr;
-    uint16_t *scale = nullptr;
     const int ps = p.c.page_size();
-    if (store) {
-        const long long at = (long long)p.lens[b] - behind;
-        if (at < 0) {
-            store = false;
-        } else if (at >= p.c.max_len()) {
-            store = false;
-            atomicOr(p.c.err, kErrBadPage);
+    // Position of token t, -1 where it has none, and the number of its page; the
+    // sequence moves on with t.
+    auto locate = [&](bool real, int at_t, int *page) {
+        if (!real || at_t < begin || at_t >= end)
+            return -1;
+        if (p.tok_start) {
+            while (at_t >= seq_end && b + 1 < p.c.batch)
+                seq_end = p.tok_start[++b + 1];
         } else {
-            uint8_t *page = kv4_page(p.c, b, int(at) >> p.c.lg_ps);
-            store = page != nullptr;
-            if (store) {
-                const int slot = int(at) & (ps - 1);
-                uint8_t *block = page + h * p.c.head_bytes<D>();
-                codes = block + slot * (D / 2);
-                scale = reinterpret_cast<uint16_t *>(block + (long long)ps * D) + slot;
-            }
+            b = at_t;
+            seq_end = at_t + 1;
+        }
+        const long long at = (long long)p.lens[b] - (seq_end - at_t);
+        if (at >= p.c.max_len()) {
+            atomicOr(p.c.err, kErrBadPage);
+            return -1;
+        }
+        if (at >= 0)
+            *page = p.c.table[(long long)b * p.c.max_pages + (int(at) >> p.c.lg_ps)];
+        return int(max(at, -1ll));
+    };
+    int page = 0, at = locate(first < stop, t, &page);
+    // (a warp's groups go round together: lanes without a row stay for the
+    // shuffles and store nothing)
+    for (int item = first; item - int(threadIdx.x / kLanes) < stop; item += kGroups) {
+        int next_t = t, next_h = h + kGroups, next_page = 0;
+        while (next_h >= p.c.kv_heads) {
+            next_h -= p.c.kv_heads;
+            ++next_t;
+        }
+        const bool more = stop - item > kGroups;
+        load(more, next_t, next_h, next_k, next_v);
+        const int next_at = locate(more, next_t, &next_page);
+
+        uint8_t *codes = nullptr;
+        uint16_t *scale = nullptr;
+        bool store = at >= 0;
+        if (store && unsigned(page) >= unsigned(p.c.num_pages)) {
+            atomicOr(p.c.err, kErrBadPage);
+            store = false;
+        }
+        if (store) {
+            const int slot = at & (ps - 1);
+            uint8_t *block = p.c.pages + (unsigned long long)unsigned(page) * p.page_stride +
+                             unsigned(h * (D + 4)) * (unsigned long long)ps;
+            codes = block + slot * (D / 2);
+            scale = reinterpret_cast<uint16_t *>(block + ps * D) + slot;
+        }
+        // Even lanes work out the key row's scale, odd ones the value row's.
+        const uint32_t top_k = row_top<D>(k), top_v = row_top<D>(v);
+        const uint32_t top = (lane & 1) ? top_v : top_k;
+        uint32_t sbits = 0x7FC0;  // NaN: the row holds a NaN or an infinity
+        float inv = 0.0f;
+        if (top < 0x7F800000u) {
+            sbits = bf16_bits(__fdiv_rn(__uint_as_float(top), 7.0f));
+            const float s = __uint_as_float(sbits << 16);
+            if (sbits != 0)
+                inv = reciprocal(s < 7.9e-31f ? s * 1.2676506002282294e30f : s);
+        }
+        const int even = threadIdx.x & 30;
+        put_row<D>(k, __shfl_sync(0xffffffffu, sbits, even), __shfl_sync(0xffffffffu, inv, even),
+                   lane, codes, scale, store);
+        put_row<D>(v, __shfl_sync(0xffffffffu, sbits, even + 1),
+                   __shfl_sync(0xffffffffu, inv, even + 1), lane, codes + ps * (D / 2), scale + ps,
+                   store);
+        t = next_t;
+        h = next_h;
+        at = next_at;
+        page = next_page;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            k[i] = next_k[i];
+            v[i] = next_v[i];
         }
     }
-    put_row<D>(k, lane, codes, scale, store);
-    put_row<D>(v, lane, codes + ps * (D / 2), scale + ps, store);
 }
 
 }  // namespace
@@ -173,12 +260,18 @@ cudaError_t launch_kv4_append(const Kv4View &c, int D, const void *k, const void
                               long long k_stride, long long v_stride, const int32_t *tok_start,
                               const int32_t *lens, int T, cudaStream_t stream)
 {
-    const AppendParams p{c, k, v, k_stride, v_stride, tok_start, lens, T};
-    const long long groups = (long long)T * c.kv_heads;
-    const int per_cta = kAppendThreads / (D / 8);
-    const long long grid = (groups + per_cta - 1) / per_cta;
-    if (grid > INT32_MAX)
+    const long long items = (long long)T * c.kv_heads;
+    const int groups = kAppendThreads / (D / 8);
+    // Four CTAs fit an SM; more items than that many groups go round.
+    const long long rounds = (items + groups - 1) / groups;  // of one CTA
+    const long long most = 4ll * device_sm_count();
+    const long long per = rounds <= most ? 1 : (rounds + most - 1) / most;
+    if (items > INT32_MAX - 2 * groups * per || k_stride > UINT32_MAX || v_stride > UINT32_MAX ||
+        c.page_stride > UINT32_MAX)
         return cudaErrorInvalidValue;
+    const AppendParams p{c, k, v, unsigned(k_stride), unsigned(v_stride), unsigned(c.page_stride),
+                         tok_start, lens, T, int(items), int(per) * groups};
+    const long long grid = (rounds + per - 1) / per;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid));
     cfg.blockDim = dim3(kAppendThreads);
