@@ -88,38 +88,33 @@ struct Span {
     int begin, end, tile0, tiles;
 };
 
-__device__ __forceinline__ Span span_of(const DecodeParams &p, int b)
+__device__ __forceinline__ Span span_of_length(const DecodeParams &p, int len)
 {
     Span s;
-    s.end = kv4_len(p.c, p.lens, b);
+    s.end = len;
     s.begin = p.q.window > 0 ? max(0, s.end - p.q.window) : 0;
     s.tile0 = s.begin / kTile;
     s.tiles = (s.end + kTile - 1) / kTile - s.tile0;
     return s;
 }
 
-// Shares: of n CTAs each takes total / n tiles, the first total % n one more;
-// warp w takes [w per, (w + 1) per) of them, per = ceil(count / warps).
-struct Share {
-    int first, count, per;
+__device__ __forceinline__ Span span_of(const DecodeParams &p, int b)
+{
+    return span_of_length(p, kv4_len(p.c, p.lens, b));
+}
+
+// `count` tiles in `n` shares: the first `more` have each + 1, the others each.
+struct Shares {
+    int each, more;
+
+    __device__ __forceinline__ Shares(int count, int n) : each(count / n), more(count - each * n) {}
+    __device__ __forceinline__ int first(int i) const { return i * each + min(i, more); }
+    __device__ __forceinline__ int of(int tile) const  // the share that holds tile
+    {
+        const int split = more * (each + 1);
+        return tile < split ? tile / (each + 1) : more + (tile - split) / each;
+    }
 };
-
-__device__ __forceinline__ Share share_of(int total, int cta, int ctas, int warps)
-{
-    const int each = total / ctas, more = total - each * ctas;
-    Share s;
-    s.first = cta * each + min(cta, more);
-    s.count = each + (cta < more);
-    s.per = (s.count + warps - 1) / warps;
-    return s;
-}
-
-__device__ __forceinline__ int cta_of(int tile, int total, int ctas)
-{
-    const int each = total / ctas, more = total - each * ctas;
-    const int split = more * (each + 1);  // tiles of the CTAs that take one more
-    return tile < split ? tile / (each + 1) : more + (tile - split) / each;
-}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1)
@@ -702,19 +697,23 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
         }
         return v;
     };
-    Share share;
-    int at, stop, b = 0, seq0 = 0, total = 0;  // the warp's first sequence, tiles before it
+    int b = 0, seq0 = 0, total = 0;  // the warp's first sequence, tiles before it
+    int len = 0;                     // its length
+    int cta_first, cta_stop;
     if (p.c.batch <= 32) {
-        const int own = tiles_of(lane);
+        const Span mine = lane < p.c.batch ? span_of(p, lane) : Span{0, 0, 0, 0};
+        const int own = mine.tiles * hg;
         if (warp == S::kWarps - 1)
             empty_rows(lane, own);
         const int incl = running_sum(own);
         total = __shfl_sync(0xffffffffu, incl, 31);
-        share = share_of(total, blockIdx.x, gridDim.x, S::kWarps);
-        at = share.first + min(share.count, warp * share.per);
-        stop = share.first + min(share.count, (warp + 1) * share.per);
+        const Shares ctas(total, gridDim.x);
+        cta_first = ctas.first(blockIdx.x);
+        cta_stop = ctas.first(blockIdx.x + 1);
+        const int at = cta_first + Shares(cta_stop - cta_first, S::kWarps).first(warp);
         b = min(31, __popc(__ballot_sync(0xffffffffu, incl <= at)));
         seq0 = __shfl_sync(0xffffffffu, incl - own, b);
+        len = __shfl_sync(0xffffffffu, mine.end, b);
     } else {
         int mine = 0, own = 0;  // own: of the thread's sequence in the first block
         for (int i = threadIdx.x; i < p.c.batch; i += kThreads) {
@@ -737,20 +736,21 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
             base += w < warp ? scan[w] : 0;
             before += scan[w];
         }
-        share = share_of(total, blockIdx.x, gridDim.x, S::kWarps);
-        at = share.first + min(share.count, warp * share.per);
-        stop = share.first + min(share.count, (warp + 1) * share.per);
+        const Shares ctas(total, gridDim.x);
+        cta_first = ctas.first(blockIdx.x);
+        cta_stop = ctas.first(blockIdx.x + 1);
+        const Shares warps(cta_stop - cta_first, S::kWarps);
         auto place = [&](int i, int lo, int n) {  // sequence i has tiles [lo, lo + n)
             for (int w = 0; w < S::kWarps; ++w) {
-                const int t = share.first + w * share.per;
-                if (w * share.per < share.count && t >= lo && t < lo + n) {
+                const int t = cta_first + warps.first(w);
+                if (t < cta_stop && t >= lo && t < lo + n) {
                     warp_b[w] = i;
                     warp_base[w] = lo;
                 }
             }
         };
         place(threadIdx.x, base + incl - own, own);
-        for (int b0 = kThreads; b0 < p.c.batch && before < share.first + share.count;
+        for (int b0 = kThreads; b0 < p.c.batch && before < cta_stop;
              b0 += kThreads) {
             own = tiles_of(b0 + threadIdx.x);
             incl = running_sum(own);
@@ -766,11 +766,15 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
             place(b0 + threadIdx.x, base + incl - own, own);
         }
         __syncthreads();
-        if (at < stop) {
+        if (cta_first + warps.first(warp) < cta_stop) {
             b = warp_b[warp];
             seq0 = warp_base[warp];
+            len = kv4_len(p.c, p.lens, b);
         }
     }
+    const Shares warps(cta_stop - cta_first, S::kWarps);
+    const int warp_first = cta_first + warps.first(warp), stop = cta_first + warps.first(warp + 1);
+    int at = warp_first;
 
     uint8_t *ring = smem + warp * (S::kStages * S::kStageBytes);
     const int worker = blockIdx.x * S::kWarps + warp;
@@ -784,10 +788,11 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
     Crossing cross{-1, 0, 0, 0};
     int end_item = -1;
     while (at < stop && fine) {
-        Span sp = span_of(p, b);
+        Span sp = span_of_length(p, len);
         while (sp.tiles * hg <= at - seq0 && b + 1 < p.c.batch) {
             seq0 += sp.tiles * hg;  // on to the sequence with tile `at`
-            sp = span_of(p, ++b);
+            len = kv4_len(p.c, p.lens, ++b);
+            sp = span_of_length(p, len);
         }
         if (sp.tiles * hg <= at - seq0)
             break;  // only if lengths change while the kernel runs
@@ -798,28 +803,39 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
         const int kvh = ig / p.groups, grp = ig - kvh * p.groups;
         const int head0 = kvh * p.rep + grp * S::kHeads;
         const int heads = min(S::kHeads, p.rep - grp * S::kHeads);
-        uint4 raw[HG][D / 32];
-        fetch_queries<D, HG>(p, b * p.q.q_stride, head0, heads, raw);
-
         // Page numbers of the next tiles, one lane each (a page of 128 tokens
         // serves two tiles); -1 for one outside the cache.
         const int lg_batch = lg_sps - 1;  // log2 of the tiles that 32 lanes cover
-        int batch0 = -1, page = -1;
+        int batch0 = n0 >> lg_batch, page = 0;
+        bool checked = false;
+        auto key_of = [&] { return ((sp.tile0 + (batch0 << lg_batch)) << 6) + (lane << lg_sps); };
+        auto wanted = [&](int j) {
+            // (pages in front of a window may have gone to other sequences)
+            return j < sp.end && j + sps > sp.begin;
+        };
+        auto look_up = [&] {
+            if (wanted(key_of()))
+                page = p.c.table[(long long)b * p.c.max_pages + (key_of() >> p.c.lg_ps)];
+            checked = false;
+        };
+        look_up();
+        uint4 raw[HG][D / 32];  // (both are on their way together)
+        fetch_queries<D, HG>(p, b * p.q.q_stride, head0, heads, raw);
         const long long head_at = kvh * p.c.head_bytes<D>();
         auto fetch = [&](int n, int s) {  // tile n of the sequence into stage s
             const int tile = sp.tile0 + n;
             if ((n >> lg_batch) != batch0) {
                 batch0 = n >> lg_batch;
-                const int j = ((sp.tile0 + (batch0 << lg_batch)) << 6) + (lane << lg_sps);
-                page = -1;
-                // (pages in front of a window may have gone to other sequences)
-                if (j < sp.end && j + sps > sp.begin) {
-                    const int pg = p.c.table[(long long)b * p.c.max_pages + (j >> p.c.lg_ps)];
-                    if (unsigned(pg) < unsigned(p.c.num_pages))
-                        page = pg;
-                    else
-                        atomicOr(p.c.err, kErrBadPage);
+                look_up();
+            }
+            if (!checked) {
+                if (!wanted(key_of())) {
+                    page = -1;
+                } else if (unsigned(page) >= unsigned(p.c.num_pages)) {
+                    page = -1;
+                    atomicOr(p.c.err, kErrBadPage);
                 }
+                checked = true;
             }
             const int i0 = (n & ((1 << lg_batch) - 1)) * per_tile;
             uint8_t *dst = ring + s * S::kStageBytes;
@@ -849,16 +865,17 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
         uint32_t good = 0;  // four bits per stage: which stretches arrive
         for (int s = 0; s < S::kStages && n0 + s < n1; ++s)
             good |= fetch(n0 + s, s) << (4 * s);
-        if (n0 > 0 && at == share.first) {
+        if (n0 > 0 && at == cta_first) {
             // (while the first tile is on its way)
-            const Share s0 = share_of(total, blockIdx.x - 1, gridDim.x, S::kWarps);
-            if (item0 >= s0.first) {
-                const int end = item0 + sp.tiles, cta1 = cta_of(end - 1, total, gridDim.x);
-                const Share s1 = share_of(total, cta1, gridDim.x, S::kWarps);
+            const Shares ctas(total, gridDim.x);
+            const int first0 = ctas.first(blockIdx.x - 1);
+            if (item0 >= first0) {
+                const int end = item0 + sp.tiles, cta1 = ctas.of(end - 1);
+                const int first1 = ctas.first(cta1);
                 cross.item = b * hg + ig;
                 cross.parts = cta1 - int(blockIdx.x) + 2;
-                cross.warp0 = (item0 - s0.first) / s0.per;
-                cross.ended = end < s1.first + min(s1.count, s1.per);
+                cross.warp0 = Shares(cta_first - first0, S::kWarps).of(item0 - first0);
+                cross.ended = end < first1 + Shares(ctas.first(cta1 + 1) - first1, S::kWarps).first(1);
             }
         }
         convert_queries<D, HG>(p, raw, qs);
@@ -897,8 +914,8 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
         p.crossing[blockIdx.x] = cross;
     // A part that no other warp of this CTA adds to needs no merge.
     const bool alone = last.item >= 0 && fine &&
-                       (warp == 0 || last.first >= share.first + warp * share.per) &&
-                       (stop == share.first + share.count || last.last <= stop);
+                       (warp == 0 || last.first >= warp_first) &&
+                       (stop == cta_stop || last.last <= stop);
     if (alone) {
         store_part<D, HG>(run, qs, p.parts + (long long)(2 * worker + 1) * p.rows * (D + 2), p.rows);
         last.item = -1;
@@ -916,7 +933,7 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
         store_part<D, HG>(run, qs, mine_at, S::kHeads);
     __syncthreads();
 #pragma unroll 1
-    for (int w = 0; w < S::kWarps && w * share.per < share.count;) {
+    for (int w = 0; w < S::kWarps && warps.first(w) < cta_stop - cta_first;) {
         const Segment s = seg[w];
         int n = 1;
         while (w + n < S::kWarps && s.item >= 0 && seg[w + n].item == s.item)
@@ -927,8 +944,7 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
             const int head0 = kvh * p.rep + grp * S::kHeads;
             const int heads = min(S::kHeads, p.rep - grp * S::kHeads);
             const bool more = w + n < S::kWarps && ended[w + n] == s.item;
-            const int from = share.first + w * share.per;
-            const int to = share.first + min(share.count, (w + n) * share.per);
+            const int from = cta_first + warps.first(w), to = cta_first + warps.first(w + n);
             const bool whole = from <= s.first && (more || to >= s.last);
             const float *first =
                 reinterpret_cast<const float *>(smem) + w * (S::kHeads * S::kPartFloats);
@@ -937,14 +953,16 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
                 p.parts + (long long)(2 * (blockIdx.x * S::kWarps + w + n)) * p.rows * (D + 2);
             for (int i = threadIdx.x; i < heads * (D / 2); i += kThreads) {
                 const int h = i / (D / 2), d = 2 * (i - h * (D / 2));
+                auto part = [&](int k) {
+                    return k < n ? first + (k * S::kHeads + h) * S::kPartFloats : tail + h * (D + 2);
+                };
                 Joined r;
-#pragma unroll 1
-                for (int k = 0; k < n + more; ++k) {
-                    const float *x = k < n ? first + (k * S::kHeads + h) * S::kPartFloats
-                                           : tail + h * (D + 2);
-                    r.add(*reinterpret_cast<const float2 *>(x + d),
-                          *reinterpret_cast<const float2 *>(x + D));
-                }
+                for (int k = 0; k < n + more; ++k)
+                    r.m = fmaxf(r.m, part(k)[D]);
+#pragma unroll 4
+                for (int k = 0; k < n + more; ++k)
+                    r.add_below(*reinterpret_cast<const float2 *>(part(k) + d),
+                                *reinterpret_cast<const float2 *>(part(k) + D));
                 if (whole) {
                     store_joined<D>(p, r, sb, head0 + h, d);
                 } else {
