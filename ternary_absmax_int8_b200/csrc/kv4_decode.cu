@@ -56,9 +56,10 @@ constexpr int kMaxCtas = 160;  // of a launch: one per SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Warps of a CTA (one CTA per SM) and ring stages per warp: as many bytes in
-// flight as shared memory holds, with registers for the heads' results. HG
-// groups of four heads share a pass over the codes.
+// Warps of a CTA (one CTA per SM) and ring stages per warp: as many as shared
+// memory and the registers for the heads' results allow (a tile is 2000 cycles
+// of latency to a warp; with 10 warps instead of 12 of D = 128 a long context
+// took 43 us, not 39). HG groups of four heads share a pass over the codes.
 template <int D, int HG>
 struct DecodeShape {
     static constexpr int kWarps = HG == 4 ? 8 : D == 128 ? 12 : 16;
@@ -932,55 +933,83 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
     if (last.item >= 0 && fine)
         store_part<D, HG>(run, qs, mine_at, S::kHeads);
     __syncthreads();
-#pragma unroll 1
-    for (int w = 0; w < S::kWarps && warps.first(w) < cta_stop - cta_first;) {
-        const Segment s = seg[w];
-        int n = 1;
-        while (w + n < S::kWarps && s.item >= 0 && seg[w + n].item == s.item)
-            ++n;
-        if (s.item >= 0) {
-            const int sb = s.item / hg, ig = s.item - sb * hg;
-            const int kvh = ig / p.groups, grp = ig - kvh * p.groups;
-            const int head0 = kvh * p.rep + grp * S::kHeads;
-            const int heads = min(S::kHeads, p.rep - grp * S::kHeads);
-            const bool more = w + n < S::kWarps && ended[w + n] == s.item;
-            const int from = cta_first + warps.first(w), to = cta_first + warps.first(w + n);
-            const bool whole = from <= s.first && (more || to >= s.last);
-            const float *first =
-                reinterpret_cast<const float *>(smem) + w * (S::kHeads * S::kPartFloats);
-            float *dst = p.parts + (long long)(2 * (blockIdx.x * S::kWarps + w) + 1) * p.rows * (D + 2);
-            const float *tail =
-                p.parts + (long long)(2 * (blockIdx.x * S::kWarps + w + n)) * p.rows * (D + 2);
-            for (int i = threadIdx.x; i < heads * (D / 2); i += kThreads) {
-                const int h = i / (D / 2), d = 2 * (i - h * (D / 2));
-                auto part = [&](int k) {
-                    return k < n ? first + (k * S::kHeads + h) * S::kPartFloats : tail + h * (D + 2);
-                };
-                Joined r;
-                for (int k = 0; k < n + more; ++k)
-                    r.m = fmaxf(r.m, part(k)[D]);
-#pragma unroll 4
-                for (int k = 0; k < n + more; ++k)
-                    r.add_below(*reinterpret_cast<const float2 *>(part(k) + d),
-                                *reinterpret_cast<const float2 *>(part(k) + D));
-                if (whole) {
-                    store_joined<D>(p, r, sb, head0 + h, d);
-                } else {
-                    *reinterpret_cast<float2 *>(dst + h * (D + 2) + d) = r.v;
-                    if (d == 0)
-                        *reinterpret_cast<float2 *>(dst + h * (D + 2) + D) = make_float2(r.m, r.l);
-                }
-            }
+    // Runs of warps whose shares ended in one item; a task is one head's 64
+    // values (32 element pairs) of a run, a warp's at a time.
+    const int item_w = lane < S::kWarps ? seg[lane].item : -1;
+    const int item_before = __shfl_up_sync(0xffffffffu, item_w, 1);
+    uint32_t starts = __ballot_sync(0xffffffffu, item_w >= 0 && (lane == 0 || item_w != item_before));
+    constexpr int kTasks = S::kHeads * (D / 64);  // of a run
+    int task = warp;
+    while (starts) {
+        if (task >= kTasks) {
+            task -= kTasks;
+            starts &= starts - 1;
+            continue;
         }
-        w += n;
+        const int w = __ffs(starts) - 1;
+        const Segment sg = seg[w];
+        const int n = __popc(__ballot_sync(0xffffffffu, item_w == sg.item));
+        const int h = task / (D / 64), d = (task % (D / 64)) * 64 + 2 * lane;
+        const int sb = sg.item / hg, ig = sg.item - sb * hg;
+        const int kvh = ig / p.groups, grp = ig - kvh * p.groups;
+        task += S::kWarps;
+        if (h >= min(S::kHeads, p.rep - grp * S::kHeads))
+            continue;
+        const bool more = w + n < S::kWarps && ended[w + n] == sg.item;
+        const int from = cta_first + warps.first(w), to = cta_first + warps.first(w + n);
+        const bool whole = from <= sg.first && (more || to >= sg.last);
+        const float *first =
+            reinterpret_cast<const float *>(smem) + (w * S::kHeads + h) * S::kPartFloats;
+        const float *tail =
+            p.parts + ((long long)(2 * (blockIdx.x * S::kWarps + w + n)) * p.rows + h) * (D + 2);
+        // lane k: part k's maximum and sum
+        float2 ml = make_float2(-INFINITY, 0.0f), x_tail = make_float2(0.0f, 0.0f);
+        if (lane < n)
+            ml = *reinterpret_cast<const float2 *>(first + lane * (S::kHeads * S::kPartFloats) + D);
+        else if (more && lane == n)
+            ml = *reinterpret_cast<const float2 *>(tail + D);
+        if (more)
+            x_tail = *reinterpret_cast<const float2 *>(tail + d);
+        Joined r;
+        r.m = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            r.m = fmaxf(r.m, __shfl_xor_sync(0xffffffffu, r.m, o));
+        const float wk = ml.x == -INFINITY ? 0.0f : ex2(ml.x - r.m);
+        r.l = wk * ml.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            r.l += __shfl_xor_sync(0xffffffffu, r.l, o);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float2 x = *reinterpret_cast<const float2 *>(
+                first + k * (S::kHeads * S::kPartFloats) + d);
+            const float f = __shfl_sync(0xffffffffu, wk, k);
+            r.v.x = fmaf(f, x.x, r.v.x);
+            r.v.y = fmaf(f, x.y, r.v.y);
+        }
+        if (more) {
+            const float f = __shfl_sync(0xffffffffu, wk, n);
+            r.v.x = fmaf(f, x_tail.x, r.v.x);
+            r.v.y = fmaf(f, x_tail.y, r.v.y);
+        }
+        if (whole) {
+            store_joined<D>(p, r, sb, kvh * p.rep + grp * S::kHeads + h, d);
+        } else {
+            float *dst =
+                p.parts + ((long long)(2 * (blockIdx.x * S::kWarps + w) + 1) * p.rows + h) * (D + 2);
+            *reinterpret_cast<float2 *>(dst + d) = r.v;
+            if (d == 0)
+                *reinterpret_cast<float2 *>(dst + D) = make_float2(r.m, r.l);
+        }
     }
 }
 
 // Joins the parts of each item that several CTAs hold, in the order of the
 // tiles. Block (c - 1, h): head h of the item that CTA c's share begins in, if
 // it began in CTA c - 1. Groups of D/2 threads take every kGroups-th part each,
-// so that all loads of a part list up to 32 long are in flight at once.
-constexpr int kCombineThreads = 256;
+// eight loads in flight at once.
+constexpr int kCombineThreads = 128;
 
 template <int D, int HG>
 __global__ void __launch_bounds__(kCombineThreads)
