@@ -538,9 +538,12 @@ tq_status tq_kv4_append(const tq_kv4_cache *cache, const uint16_t *k_bf16,
  * j <= p, j > p - window where window > 0:
  *   z_j = scale * (q . k_j),  out = sum_j softmax(z)_j v_j,
  *   lse = log(sum_j exp(z_j))   (natural logarithm)
- * A query that sees nothing has out = 0 and lse = -infinity. q . codes is an
- * fp32 sum: query values are finite and at most 2^117 in magnitude, else the
- * rows of that head and token may be NaN.
+ * A query that sees nothing has out = 0 and lse = -infinity. Scores are fp32
+ * numbers of any finite query values; a score out of fp32's range, or a NaN or
+ * an infinity among a row's query values, makes that row NaN.
+ * Roundings: scores and sums in fp32; a weight times its value's scale once to
+ * fp16 (tq_kv4_decode, against the largest scale of 64 tokens) or bf16
+ * (tq_kv4_prefill); out to bf16.
  */
 typedef struct tq_kv4_query {
     const uint16_t *q;       /* device, bf16 [T, q_heads, head_dim], 16-byte aligned (tq_rope

@@ -73,9 +73,8 @@ def test_strides_no_lse_and_padded_pages(cuda_device, decode):
 @pytest.mark.parametrize("spread,scale", [(30.0, 0.5), (1e-6, 1.0), (1e18, 1e-18), (2e35, 1e-35)])
 def test_sharp_flat_and_huge_queries(cuda_device, decode, spread, scale):
     """One key takes all, all keys weigh the same, query values beyond fp16.
-    A score is an fp32 sum of up to 128 products with codes up to 7, and
-    128 * 7 * 3.8e35 is FLT_MAX: 2e35 is near the largest query value that the
-    call takes (2^117 = 1.7e35 for any codes; these codes are smaller)."""
+    (2e35: a sum of 128 products with codes up to 7 is still below FLT_MAX, for
+    kernels that take queries as they are.)"""
     rng = np.random.default_rng(4)
     n = [1, 1] if decode else [70, 2]
     cache = Cache(rng, [200, 131], 2, 128, 64)
