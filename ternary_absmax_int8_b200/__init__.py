@@ -204,9 +204,6 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        if torch.cuda.is_initialized():
-            # the current stream's handle, without building a Stream object around it
-            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
         if not torch.cuda.is_available():
             return None
         return torch.cuda.current_stream().cuda_stream
@@ -372,16 +369,29 @@ def _device() -> int:
     return -2
 
 
+def _here(stream):
+    """The current CUDA device and the handle of `stream` (of the current one if None): what a
+    call needs to know, looked up once."""
+    import torch
+    if not torch.cuda.is_initialized():
+        return _device(), _stream(stream)
+    device = torch.cuda.current_device()
+    if stream is None:
+        # without building a Stream object around it
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    return device, _stream(stream)
+
+
 def _gpu_ptr(t, size: int, device: int):
     """Pointer of a tensor of `size`-byte elements on CUDA device `device`, the current one (an
     int or None passes through); a tensor elsewhere is refused, as the kernel would run here."""
     if t is None or isinstance(t, int):
         return t
+    if t.get_device() == device and t.element_size() == size:
+        return t.data_ptr()
     if t.element_size() != size:
         raise TQError(4, f"a tensor of {size}-byte elements is wanted, not {t.dtype}")
-    if t.get_device() != device:
-        raise TQError(4, f"a tensor on {t.device}: tensors must be on the current CUDA device")
-    return t.data_ptr()
+    raise TQError(4, f"a tensor on {t.device}: tensors must be on the current CUDA device")
 
 
 def make_rope_rows(rows, head_dim: int):
@@ -401,11 +411,11 @@ def make_rope_rows(rows, head_dim: int):
 def tq_rope(rows, pos, inv_freq, sections, T: int, head_dim: int, rot_dim: int, flags: int = 0,
             pos_stride: int = 0, stream=None) -> None:
     """Rotary positions of the rows in a make_rope_rows table; pos int32 [len(sections), T]."""
-    dev = _device()
+    dev, stream = _here(stream)
     n = len(sections)
     _check(_load().tq_rope(rows, len(rows), _gpu_ptr(pos, 4, dev), int(pos_stride) or int(T),
                            _gpu_ptr(inv_freq, 4, dev), (_i * n)(*sections), n, int(T), int(head_dim),
-                           int(rot_dim), int(flags), _stream(stream)))
+                           int(rot_dim), int(flags), stream))
 
 
 def tq_kv4_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
@@ -425,11 +435,11 @@ def make_kv4_cache(pages=None, page_table=None, num_pages: int = 0, page_size: i
 def tq_kv4_append(cache, k_bf16, v_bf16, k_f32, v_f32, tok_start, lens, T: int, k_stride: int = 0,
                   v_stride: int = 0, stream=None) -> None:
     """Quantise new keys and values into the cache's pages (one of the two pairs)."""
-    dev = _device()
+    dev, stream = _here(stream)
     _check(_load().tq_kv4_append(ctypes.byref(cache), _gpu_ptr(k_bf16, 2, dev), _gpu_ptr(v_bf16, 2, dev),
                                  _gpu_ptr(k_f32, 4, dev), _gpu_ptr(v_f32, 4, dev), int(k_stride),
                                  int(v_stride), _gpu_ptr(tok_start, 4, dev), _gpu_ptr(lens, 4, dev), int(T),
-                                 _stream(stream)))
+                                 stream))
 
 
 def tq_kv4_decode_workspace(cache, q_heads: int) -> int:
@@ -455,18 +465,18 @@ def tq_kv4_decode(cache, q, lens, out, lse, q_heads: int, scale: float, window: 
                   workspace=None, workspace_bytes: int = 0, q_stride: int = 0,
                   out_stride: int = 0, stream=None) -> None:
     """Attention of one new token per sequence over the cache."""
-    dev = _device()
+    dev, stream = _here(stream)
     query = _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride)
     _check(_load().tq_kv4_decode(ctypes.byref(cache), query, _gpu_ptr(lens, 4, dev),
-                                 _gpu_ptr(workspace, 1, dev), int(workspace_bytes), _stream(stream)))
+                                 _gpu_ptr(workspace, 1, dev), int(workspace_bytes), stream))
 
 
 def tq_kv4_prefill(cache, q, tok_start, lens, out, lse, T: int, q_heads: int, scale: float,
                    window: int = 0, workspace=None, workspace_bytes: int = 0, q_stride: int = 0,
                    out_stride: int = 0, stream=None) -> None:
     """Attention of any number of new tokens per sequence over the cache."""
-    dev = _device()
+    dev, stream = _here(stream)
     query = _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride)
     _check(_load().tq_kv4_prefill(ctypes.byref(cache), query, _gpu_ptr(tok_start, 4, dev),
                                   _gpu_ptr(lens, 4, dev), int(T), _gpu_ptr(workspace, 1, dev),
-                                  int(workspace_bytes), _stream(stream)))
+                                  int(workspace_bytes), stream))
