@@ -472,6 +472,7 @@ tq_status tq_rope(const tq_rope_rows *rows, int n, const int32_t *pos, int64_t p
  * absmax per token, here per token and key/value head.
  *   s = bf16(fl32(absmax / 7));  code = the whole number nearest to x / s
  *   (ties to even, decided exactly), -7..7;  value = code * s.
+ *   (|x / s| < 7.5 but where s is subnormal; there codes end at 7.)
  *   A row of zeros (or one whose s rounds to 0) has s = 0 and codes 0. A row
  *   that holds a NaN or an infinity has s = NaN and codes 0: attention that
  *   sees it gives NaN, attention that does not is unharmed.

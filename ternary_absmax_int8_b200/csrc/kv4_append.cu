@@ -6,7 +6,7 @@
 // scale is bf16, the range of fp32 at 2 bytes: fp16 would overflow or lose
 // small rows, fp32 would add 3% to every later read of the cache. Codes are
 // taken against the rounded scale, so its rounding (2^-9) costs no accuracy
-// beyond the code's own half step; |x / s| stays below 7.04.
+// beyond the code's own half step; |x / s| stays below 7.04 (but for subnormal s).
 //
 // Bound by HBM (K and V read once, D + 4 bytes a token and head written): a
 // group of D/8 lanes holds one (token, head) pair of rows, 8 values of each
@@ -122,12 +122,14 @@ __device__ __forceinline__ void put_row(const float (&x)[8], uint32_t sbits, flo
     if (inv != 0.0f) {
         float s = __uint_as_float(sbits << 16);
         if (s < 7.9e-31f) {
-            // below 2^-100 all is lifted by 2^100, as 1 / s might be infinite
+            // below 2^-100 all is lifted by 2^100, as 1 / s might be infinite;
+            // a subnormal s may be so far below absmax / 7 that codes end at 7
             constexpr float kLift = 1.2676506002282294e30f;
+            const float top = 7.0f * (s * kLift);
             float y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                y[i] = x[i] * kLift;
+                y[i] = fminf(fmaxf(x[i] * kLift, -top), top);
             packed = pack_codes(y, s * kLift, inv);
         } else {
             packed = pack_codes(x, s, inv);

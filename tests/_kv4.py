@@ -44,6 +44,7 @@ def quantise(x):
     s = bf16_round((amax / np.float32(7)).astype(np.float32)).reshape(amax.shape)
     d = np.where(s > 0, s, 1).astype(np.float64)[..., None]
     c = np.rint(np.where(bad[..., None], 0, x).astype(np.float64) / d) * (s > 0)[..., None]
+    c = np.clip(c, -7, 7)  # (a subnormal s may be far below absmax / 7)
     return c.astype(np.int64), np.where(bad, np.float32(np.nan), s)
 
 

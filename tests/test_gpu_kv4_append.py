@@ -115,6 +115,25 @@ def test_append_borders(cuda_device, f32):
     assert np.array_equal(gs[~np.isnan(gs)], ws[~np.isnan(ws)])
 
 
+@pytest.mark.parametrize("f32", [True, False])
+def test_append_subnormal_scales(cuda_device, f32):
+    """Rows of a few of bf16's last steps, 2^-133: s rounds to 1 of them for all
+    up to 10, and codes end at 7."""
+    D, hk, T = 64, 1, 64
+    rng = np.random.default_rng(13)
+    k = np.empty((T, hk, D), np.float32)
+    for t in range(T):
+        k[t] = rng.integers(-t, t + 1, (hk, D)) * np.float32(2.0 ** -133)
+        k[t, :, 3] = t * np.float32(2.0 ** -133)
+    v = -k[::-1].copy()
+    assert k.max() == np.float32(63 * 2.0 ** -133)  # the host does not flush them
+    cache = Cache(rng, [T], hk, D, 64)
+    c, keep = cache.on_gpu()
+    append(c, keep, k, v, f32, [T], [T])
+    put(cache, k, v, [T], [T])
+    assert np.array_equal(keep[0].cpu().numpy(), cache.bytes())
+
+
 def test_append_bad_pages_are_reported_and_skipped(cuda_device):
     rng = np.random.default_rng(11)
     lens = [70, 5]
