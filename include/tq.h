@@ -540,8 +540,9 @@ tq_status tq_kv4_append(const tq_kv4_cache *cache, const uint16_t *k_bf16,
  *   z_j = scale * (q . k_j),  out = sum_j softmax(z)_j v_j,
  *   lse = log(sum_j exp(z_j))   (natural logarithm)
  * A query that sees nothing has out = 0 and lse = -infinity. Scores are fp32
- * numbers of any finite query values; a score out of fp32's range, or a NaN or
- * an infinity among a row's query values, makes that row NaN.
+ * numbers, of query values that are 0 or at least 2^-90 (no upper limit) with
+ * |k| and scale |q| up to 2^90. A NaN or an infinity among a row's query
+ * values, or a score beyond fp32's largest number, makes that row NaN.
  * Roundings: scores and sums in fp32; a weight times its value's scale once to
  * fp16 (tq_kv4_decode, against the largest scale of 64 tokens) or bf16
  * (tq_kv4_prefill); out to bf16.

@@ -282,6 +282,7 @@ __device__ __forceinline__ void convert_queries(const DecodeParams &p,
         // the unit, scale and the change to base 2; an infinite or NaN query
         // makes all of its head's scores NaN
         mul[j] = __uint_as_float(uint32_t(k - 21 + 127) << 23) * (p.q.scale * kLog2e);
+        mul[j] = fmaxf(mul[j], 1.40129846e-45f);  // no zero, which masks would meet
         if (top >= 0x7F800000u)
             mul[j] = NAN;
         q.mul[j] = __shfl_sync(0xffffffffu, mul[j], 8 * t);

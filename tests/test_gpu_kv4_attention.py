@@ -86,6 +86,21 @@ def test_sharp_flat_and_huge_queries(cuda_device, decode, spread, scale):
 
 
 @pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("scale", [0.1, 2.0 ** -30, 2.0 ** -90])
+def test_zero_queries_weigh_all_keys_the_same(cuda_device, decode, scale):
+    """Padding rows of zeros, whose scores are 0 whatever the scale, beside keys
+    that a row does not see."""
+    rng = np.random.default_rng(14)
+    lens, n = [70, 200, 3], ([1] * 3 if decode else [70, 20, 1])
+    cache = Cache(rng, lens, 2, 128, 64)
+    c, keep = cache.on_gpu()
+    q = np.zeros((sum(n), 8, 128), np.float32)
+    q[0, 0] = 1.0
+    got = run_attention(c, keep, q, lens, n, scale, 30, decode=decode)
+    assert_attention(got, attention(cache, q, n, scale, 30))
+
+
+@pytest.mark.parametrize("decode", [True, False])
 def test_scales_of_any_size(cuda_device, decode):
     """Key and value rows from 2^-40 to 2^40, neighbours in one tile."""
     rng = np.random.default_rng(5)
