@@ -500,9 +500,9 @@ typedef struct tq_kv4_cache {
                                   least tq_kv4_page_bytes; 0: tq_kv4_page_bytes */
     int num_pages;
     int page_size;             /* tokens: 16, 32, 64 or 128 */
-    int kv_heads;
+    int kv_heads;              /* 1..1024 */
     int head_dim;              /* 64 or 128 */
-    int batch;                 /* sequences */
+    int batch;                 /* sequences, 0..65536 */
     int max_pages;             /* entries of a table row; max_pages * page_size < 2^30 */
 } tq_kv4_cache;
 
@@ -525,8 +525,9 @@ size_t tq_kv4_page_bytes(int page_size, int kv_heads, int head_dim);
  *             lens - 1. Tokens with a negative position are dropped (a
  *             sequence of length 0 in a padded batch).
  * Two tokens of one call must not share a slot (tables that name one page
- * twice where both write). One launch; waits for the previous kernel on the
- * stream before it touches memory.
+ * twice where both write). T * kv_heads is at most 2^30, strides are below
+ * 2^32 (TQ_ERR_UNSUPPORTED beyond). One launch; waits for the previous kernel
+ * on the stream before it touches memory.
  */
 tq_status tq_kv4_append(const tq_kv4_cache *cache, const uint16_t *k_bf16,
                         const uint16_t *v_bf16, const float *k_f32, const float *v_f32,
@@ -569,7 +570,9 @@ typedef struct tq_kv4_query {
  *              the GPU (two streams, two graphs replayed at once) need one
  *              each.
  * Results do not depend on the order in which SMs finish: the same inputs
- * give the same bits on every run.
+ * give the same bits on every run. batch * kv_heads * max_pages * page_size is
+ * below 2^37 (a sixteenth of that per 16 query heads of a key/value head more;
+ * TQ_ERR_UNSUPPORTED beyond).
  */
 tq_status tq_kv4_decode(const tq_kv4_cache *cache, const tq_kv4_query *query,
                         const int32_t *lens, void *workspace, size_t workspace_bytes,
@@ -581,6 +584,8 @@ tq_status tq_kv4_decode(const tq_kv4_cache *cache, const tq_kv4_query *query,
  * tok_start as in tq_kv4_append (required). Rows outside [tok_start[0],
  * tok_start[batch]) are neither read nor written.
  *   workspace  as in tq_kv4_decode, tq_kv4_prefill_workspace bytes for T rows.
+ * T times the query heads of a key/value head is at most 2^30, as is a 256th
+ * of that, and the batch, times kv_heads (TQ_ERR_UNSUPPORTED beyond).
  */
 tq_status tq_kv4_prefill(const tq_kv4_cache *cache, const tq_kv4_query *query,
                          const int32_t *tok_start, const int32_t *lens, int T, void *workspace,

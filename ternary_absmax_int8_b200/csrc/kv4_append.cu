@@ -268,9 +268,6 @@ cudaError_t launch_kv4_append(const Kv4View &c, int D, const void *k, const void
     const long long rounds = (items + groups - 1) / groups;  // of one CTA
     const long long most = 4ll * device_sm_count();
     const long long per = rounds <= most ? 1 : (rounds + most - 1) / most;
-    if (items > INT32_MAX - 2 * groups * per || k_stride > UINT32_MAX || v_stride > UINT32_MAX ||
-        c.page_stride > UINT32_MAX)
-        return cudaErrorInvalidValue;
     const AppendParams p{c, k, v, unsigned(k_stride), unsigned(v_stride), unsigned(c.page_stride),
                          tok_start, lens, T, int(items), int(per) * groups};
     const long long grid = (rounds + per - 1) / per;

@@ -43,16 +43,4 @@ __device__ __forceinline__ int kv4_len(const Kv4View &c, const int32_t *lens, in
     return max(n, 0);
 }
 
-// First byte of page `index` of sequence b, or null (and the error reported)
-// where the table names a page outside the cache.
-__device__ __forceinline__ uint8_t *kv4_page(const Kv4View &c, int b, int index)
-{
-    const int pg = c.table[(long long)b * c.max_pages + index];
-    if (unsigned(pg) >= unsigned(c.num_pages)) {
-        atomicOr(c.err, kErrBadPage);
-        return nullptr;
-    }
-    return c.pages + (long long)pg * c.page_stride;
-}
-
 }  // namespace tq

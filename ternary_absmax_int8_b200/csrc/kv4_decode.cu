@@ -1140,8 +1140,6 @@ cudaError_t launch_kv4_decode(const Kv4View &c, int D, const Kv4Query &q, const 
                               void *workspace, cudaStream_t stream)
 {
     const DecodePlan plan = plan_decode(c, D, q.q_heads);
-    if (plan.items > INT32_MAX || plan.tiles > INT32_MAX - kTile)
-        return cudaErrorInvalidValue;  // tiles are counted in 32 bits
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     DecodeParams p;
     p.c = c;

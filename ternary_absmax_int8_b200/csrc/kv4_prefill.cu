@@ -1061,9 +1061,6 @@ cudaError_t launch_kv4_prefill(const Kv4View &c, int D, const Kv4Query &q,
                                void *workspace, cudaStream_t stream)
 {
     const PrefillPlan plan = plan_prefill(c, D, q.q_heads, T);
-    if ((long long)T * plan.rep > INT32_MAX - kRows ||
-        (long long)plan.units * c.kv_heads * plan.splits > INT32_MAX)
-        return cudaErrorInvalidValue;  // rows and CTAs are counted in 32 bits
     PrefillParams p;
     p.c = c;
     p.q = q;

@@ -637,8 +637,14 @@ tq_status tq_kv4_append(const tq_kv4_cache *cache, const uint16_t *k_bf16,
     const long long packed = (long long)cache->kv_heads * cache->head_dim;
     long long ks, vs;
     if ((st = check_rows(fn, "k", k, k_stride, packed, f32 ? 4 : 2, &ks)) != TQ_OK ||
-        (st = check_rows(fn, "v", v, v_stride, packed, f32 ? 4 : 2, &vs)) != TQ_OK ||
-        (st = kv4_error_word(fn, &c)) != TQ_OK)
+        (st = check_rows(fn, "v", v, v_stride, packed, f32 ? 4 : 2, &vs)) != TQ_OK)
+        return st;
+    // rows are counted, and strides held, in 32 bits
+    if ((long long)T * cache->kv_heads > (1ll << 30) || ks > UINT32_MAX || vs > UINT32_MAX ||
+        c.page_stride > UINT32_MAX)
+        return fail(TQ_ERR_UNSUPPORTED, "%s: T=%d rows of %d heads, strides %lld, %lld, "
+                    "page_stride %lld", fn, T, cache->kv_heads, ks, vs, c.page_stride);
+    if ((st = kv4_error_word(fn, &c)) != TQ_OK)
         return st;
     cudaError_t e = tq::launch_kv4_append(c, cache->head_dim, k, v, f32, ks, vs, tok_start, lens,
                                           T, stream);
@@ -698,6 +704,11 @@ tq_status tq_kv4_decode(const tq_kv4_cache *cache, const tq_kv4_query *query,
         return fail(TQ_ERR_NULL, "%s: lens is NULL", fn);
     if (!aligned(lens, 4))
         return fail(TQ_ERR_ALIGN, "%s: lens must be 4-byte aligned", fn);
+    // tiles of 64 keys for up to 16 query heads are counted in 32 bits
+    const long long groups = (query->q_heads / cache->kv_heads + 15) / 16;
+    if (groups * cache->kv_heads * cache->batch * ((c.max_len() + 63) / 64) > (1ll << 31) - 128)
+        return fail(TQ_ERR_UNSUPPORTED, "%s: %d sequences of up to %d keys, %d key/value heads", fn,
+                    cache->batch, c.max_len(), cache->kv_heads);
     if ((st = kv4_error_word(fn, &c)) != TQ_OK)
         return st;
     cudaError_t e = tq::launch_kv4_decode(c, cache->head_dim, q, lens, workspace, stream);
@@ -727,6 +738,10 @@ tq_status tq_kv4_prefill(const tq_kv4_cache *cache, const tq_kv4_query *query,
         return fail(TQ_ERR_NULL, "%s: tok_start or lens is NULL", fn);
     if (!aligned(lens, 4) || !aligned(tok_start, 4))
         return fail(TQ_ERR_ALIGN, "%s: lens and tok_start must be 4-byte aligned", fn);
+    // a head's rows, and the CTAs of 256 of them, are counted in 32 bits
+    const long long rows = (long long)T * (query->q_heads / cache->kv_heads);
+    if (rows > (1ll << 30) || (rows / 256 + cache->batch) * cache->kv_heads > (1ll << 30))
+        return fail(TQ_ERR_UNSUPPORTED, "%s: T=%d tokens of %d query heads", fn, T, query->q_heads);
     if ((st = kv4_error_word(fn, &c)) != TQ_OK)
         return st;
     cudaError_t e = tq::launch_kv4_prefill(c, cache->head_dim, q, tok_start, lens, T, workspace,

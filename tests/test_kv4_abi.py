@@ -33,7 +33,8 @@ def decode(c=None, q=P, lens=P, out=P, lse=P, hq=20, scale=0.1, window=0, ws=P,
                      stream=0, **kw)
 
 
-def prefill(c=None, q=P, start=P, lens=P, out=P, lse=P, T=7, hq=20, scale=0.1, window=0, ws=P,            size=1 << 40, **kw):
+def prefill(c=None, q=P, start=P, lens=P, out=P, lse=P, T=7, hq=20, scale=0.1, window=0,
+            ws=P, size=1 << 40, **kw):
     tq.tq_kv4_prefill(c or cache(), q, start, lens, out, lse, T, hq, scale, window,
                       ws, size, stream=0, **kw)
 
@@ -185,3 +186,17 @@ def test_structs_match_the_header():
     assert ctypes.sizeof(tq.TqRopeRows) == 56
     assert ctypes.sizeof(tq.TqKv4Cache) == 48
     assert ctypes.sizeof(tq.TqKv4Query) == 56
+
+
+@pytest.mark.parametrize("fn,kw", [
+    (append, dict(T=(1 << 30) // 5 + 1)),
+    (append, dict(k_stride=1 << 32)),
+    (append, dict(v_stride=1 << 32)),
+    (append, dict(c=cache(page_stride=1 << 32))),
+    (decode, dict(c=cache(batch=65536, max_pages=1 << 16))),
+    (decode, dict(c=cache(batch=4096, kv_heads=1, max_pages=1 << 18), hq=17)),
+    (prefill, dict(T=(1 << 28) + 1)),
+    (prefill, dict(T=1 << 29, c=cache(kv_heads=1024), hq=1024)),
+])
+def test_counts_beyond_32_bits_are_refused(fn, kw):
+    refused("TQ_ERR_UNSUPPORTED", fn, **kw)
