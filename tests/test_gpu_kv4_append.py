@@ -166,3 +166,31 @@ def test_append_far_pages(cuda_device):
     append(c, keep, k, v, False, [10, 2], [200, 3])
     put(cache, k, v, [10, 2], [200, 3])
     assert np.array_equal(keep[0][lead:].cpu().numpy(), cache.bytes())
+
+
+def test_append_of_many_sequences(cuda_device):
+    """More (token, head) pairs than the GPU takes at once, sequences of 0 to 3
+    tokens and one long one, tokens beyond tok_start's end ignored."""
+    rng = np.random.default_rng(21)
+    n = rng.integers(0, 4, 700)
+    n[::5] = 0
+    n[300] = 900
+    lens = n + rng.integers(0, 20, 700)
+    cache = Cache(rng, lens.tolist(), 9, 64, 16)
+    c, keep = cache.on_gpu()
+    T = int(n.sum()) + 5
+    k, v = rows(rng, T, 9, 64, False), rows(rng, T, 9, 64, False)
+    append(c, keep, k, v, False, n.tolist(), lens.tolist())
+    put(cache, k, v, n, lens)
+    assert np.array_equal(keep[0].cpu().numpy(), cache.bytes())
+    assert tq.tq_device_error() == 0
+
+
+def test_append_to_no_pages(cuda_device):
+    """Tables of no entry: tokens of empty sequences are dropped, others reported."""
+    rng = np.random.default_rng(22)
+    k, v = rows(rng, 2, 1, 64, False), rows(rng, 2, 1, 64, False)
+    c = tq.make_kv4_cache(page_size=16, kv_heads=1, head_dim=64, batch=2)
+    for lens, error in (([0, 0], 0), ([0, 3], 2)):
+        append(c, None, k, v, False, [1, 1], lens)
+        assert tq.tq_device_error(reset=True) == error

@@ -229,3 +229,123 @@ def test_far_pages(cuda_device, decode):
     q = queries(rng, sum(n), 20, 128)
     got = run_attention(c, keep, q, lens, n, 0.1, decode=decode)
     assert_attention(got, attention(cache, q, n, 0.1))
+
+
+@pytest.mark.parametrize("D,rep,batch", [(128, 4, 33), (128, 1, 450), (64, 9, 300), (64, 2, 1100)])
+def test_decode_of_many_sequences(cuda_device, D, rep, batch):
+    """More sequences than a warp has lanes, or a CTA threads: empty ones first,
+    last and in long runs, one far longer than the others."""
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, 100, batch)
+    lens[rng.integers(0, 2, batch) == 0] = 0
+    lens[:3] = lens[-2:] = 0
+    lens[batch // 3:batch // 3 + 20] = 0
+    lens[batch - 5] = 900
+    check(rng, lens.tolist(), [1] * batch, 1, rep, D, 32)
+
+
+def test_prefill_of_many_sequences(cuda_device):
+    rng = np.random.default_rng(15)
+    lens = rng.integers(-1, 40, 1100)
+    n = np.minimum(np.maximum(lens, 0), rng.integers(0, 4, 1100))
+    n[::7] = 0
+    n[600], lens[600] = 300, 310
+    check(rng, lens.tolist(), n.tolist(), 1, 2, 64, 16, decode=False)
+
+
+@pytest.mark.parametrize("D,n,window", [(128, [7, 0, 1], 0), (64, [5, 9, 0], 0),
+                                        (64, [33, 2, 2], 70), (128, [3, 3, 3], 1)])
+def test_few_rows_over_a_long_cache(cuda_device, D, n, window):
+    """Key tiles in parts that are joined; parts that no row of a sequence sees."""
+    rng = np.random.default_rng(16)
+    check(rng, [2000, 130, 4], n, 2, 4, D, 64, window, decode=False)
+
+
+@pytest.mark.parametrize("decode", [True, False])
+def test_caches_without_pages(cuda_device, decode):
+    """No page, or tables of no entry: all sequences empty, or reported."""
+    n = [1, 1] if decode else [3, 2]
+    q = queries(np.random.default_rng(17), sum(n), 4, 64)
+    table = torch.zeros((2, 2), dtype=torch.int32, device="cuda")
+    for kw in (dict(max_pages=0), dict(max_pages=2, page_table=table)):
+        c = tq.make_kv4_cache(num_pages=0, page_size=16, kv_heads=2, head_dim=64, batch=2, **kw)
+        for lens, error in (([0, 0], 0), ([0, 20], 2)):
+            out, lse = run_attention(c, None, q, lens, n, 0.1, decode=decode)
+            assert (out == 0).all() and np.isneginf(lse).all()
+            assert tq.tq_device_error(reset=True) == error
+
+
+def test_prefill_of_fewer_rows_than_tok_start_names(cuda_device):
+    """tok_start beyond T: rows up to T only, at the positions they have in all."""
+    rng = np.random.default_rng(18)
+    cache = Cache(rng, [90], 1, 128, 64)
+    c, keep = cache.on_gpu()
+    q = queries(rng, 40, 4, 128)
+    ref = attention(cache, q, [40], 0.1)
+    f = dict(device="cuda", dtype=torch.int32)
+    out = torch.full((40, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((40, 4), 7.0, device="cuda")
+    size = tq.tq_kv4_prefill_workspace(c, 4, 25)
+    ws = torch.empty(max(16, size), dtype=torch.uint8, device="cuda")
+    tq.tq_kv4_prefill(c, torch.from_numpy(q).cuda().bfloat16(), torch.tensor([0, 40], **f),
+                      torch.tensor([90], **f), out, lse, 25, 4, 0.1, 0, ws, size)
+    torch.cuda.synchronize()
+    assert (out[25:] == 7).all() and (lse[25:] == 7).all()
+    got = (out[:25].double().cpu().numpy(), lse[:25].double().cpu().numpy())
+    assert_attention(got, tuple(x[:25] for x in ref))
+
+
+@pytest.mark.parametrize("decode", [True, False])
+def test_shared_pages(cuda_device, decode):
+    """Sequences with a common beginning, whose tables name the same pages."""
+    rng = np.random.default_rng(19)
+    lens, n = [130, 129, 128], ([1] * 3 if decode else [60, 1, 3])
+    cache = Cache(rng, lens, 3, 128, 32)
+    cache.table[1, :4] = cache.table[2, :4] = cache.table[0, :4]
+    c, keep = cache.on_gpu()
+    q = queries(rng, sum(n), 3, 128)
+    got = run_attention(c, keep, q, lens, n, 0.1, decode=decode)
+    assert_attention(got, attention(cache, q, n, 0.1))
+
+
+@pytest.mark.parametrize("decode", [True, False])
+def test_two_graphs_at_once(cuda_device, decode):
+    """Two captured calls with a workspace each, replayed on two streams: the
+    bits of calls that run alone."""
+    rng = np.random.default_rng(20)
+    lens, hq = [3000, 500], 8
+    T = 2 if decode else 40
+    cache = Cache(rng, lens, 2, 64, 64)
+    c, keep = cache.on_gpu()
+    f = dict(device="cuda", dtype=torch.int32)
+    lens_g, start_g = torch.tensor(lens, **f), torch.tensor([0, T - 1, T], **f)
+    size = max(16, tq.tq_kv4_decode_workspace(c, hq) if decode
+               else tq.tq_kv4_prefill_workspace(c, hq, T))
+    runs = []
+    for _ in range(2):
+        q = torch.from_numpy(queries(rng, T, hq, 64)).cuda().bfloat16()
+        out = torch.empty((T, hq, 64), dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty((T, hq), device="cuda")
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+        def call(q=q, out=out, lse=lse, ws=ws):
+            if decode:
+                tq.tq_kv4_decode(c, q, lens_g, out, lse, hq, 0.1, 0, ws, size)
+            else:
+                tq.tq_kv4_prefill(c, q, start_g, lens_g, out, lse, T, hq, 0.1, 0, ws, size)
+
+        call()
+        torch.cuda.synchronize()
+        alone = out.clone(), lse.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(4):
+                call()
+        runs.append((graph, torch.cuda.Stream(), out, lse, alone, (q, ws)))
+    for _ in range(5):
+        for graph, stream, out, lse, alone, _ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for graph, stream, out, lse, alone, _ in runs:
+            assert torch.equal(out, alone[0]) and torch.equal(lse, alone[1])
