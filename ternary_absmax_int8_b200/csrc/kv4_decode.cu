@@ -39,6 +39,13 @@
 // done. Then the warps of an SM that ended in one sequence are merged in
 // shared memory, and kv4_combine_kernel joins what several SMs hold of one
 // sequence, in a fixed order.
+//
+// Measured (20 heads on 5 of 128, pages of 64): one sequence of 777 tokens
+// 7.2 us; 24 of up to 8191 (65 MB) 22.8 us, 2.8 TB/s; one of 262143 (173 MB)
+// 38.5 us, 4.5 TB/s. Of the long call the start (lengths, page numbers, first
+// copies) takes 2.7 us, merge and join 4; between them it runs at 6 TB/s with
+// the issue slots 57%, ALUs 53% and matrix pipes 28% busy. The batch's tiles are
+// a third of that, and its start and end, with more joins, the same.
 #include <algorithm>
 
 #include "kv4_common.cuh"

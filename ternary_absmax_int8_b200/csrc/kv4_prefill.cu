@@ -13,12 +13,10 @@
 // so the scores and the logarithm of the sum are as exact as fp32 sums. Values
 // are their codes (exact in bf16); a weight times its value's scale is rounded
 // to bf16 once (2^-8: fp16's range would not do, as rows that do not see a key
-// share its tile). Folding the value scales into the values instead, another
-// bf16 rounding, is cheaper in the softmax but made results a fourth worse.
-// Per pair of row tiles and key tile (D = 128) the tensor core needs 4 x 512
-// cycles, the 2 x 16384 exponentials 2048 at 16 a cycle, shared memory about
-// 2300 (operands 1536, expanded codes 512, scales 256): nothing has slack, so
-// each runs in warps of its own:
+// share its tile). Folding the value scales into the values instead is cheaper
+// in the softmax, but a second bf16 rounding of every product.
+//
+// Each runs in warps of its own:
 //   warps 0-3, 4-7  softmax of row tile 0, 1 (also the final division)
 //   warps 8-11      codes -> 16-bit operands, swizzled for the MMA
 //   warps 12, 14    issue the MMAs of row tile 0, 1
@@ -26,6 +24,22 @@
 //                   tiles ahead
 // The running maximum may lag by a factor 2^8 (weights up to 256 in fp32 and
 // bf16 lose nothing): results in tensor memory are scaled anew only beyond.
+//
+// What bounds it: the softmax. Per pair of row tiles and key tile (D = 128) the
+// tensor core needs 4 x 512 cycles, the 2 x 16384 exponentials 2048 at 16 a
+// cycle, shared memory about 2300 (operands 1536, expanded codes 512, scales
+// 256), all instructions about 2600 issue slots of each scheduler; but a pair of
+// tiles takes 4800, as the two softmax warps of a scheduler do not cover the
+// latencies of their own chain (scores from tensor memory, maximum, exponentials,
+// weights back), and a CTA's start and end take 17000 together. A prompt of 8192
+// tokens (20 heads on 5, D = 128; 344 GFLOP) takes 380 us, 905 TFLOP/s, 55% of a
+// plain library product's rate (tensor pipe 39% busy, issue slots 51%, exponentials
+// 41% over 4096 tokens). What was tried, in us for that prompt: scores of whole
+// tiles, not ahead 519, of half tiles two ahead 422 (380 with all heads' long
+// units first); four softmax warpgroups 490 where two took 449; the next scores
+// fetched before the exponentials 534 then (spills); registers dealt anew between
+// the roles 386; the row tiles' softmax taking turns 394; a part of the
+// exponentials as polynomials 387 and more; waits that sleep longer 395.
 //
 // Few rows over a long cache are split along the keys, into parts that
 // kv4_prefill_join_kernel adds up in order.
@@ -376,7 +390,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     // Units are counted from the call's last row, and their heads and parts stand
     // next to each other: the CTAs that see most keys start first. (With one
     // head's units after the other's, the last head's long ones start when SMs
-    // run dry: 426 us instead of 370 for 8192 tokens.)
+    // run dry: 422 us instead of 380 for 8192 tokens.)
     const int kvh = blockIdx.x % p.c.kv_heads, item = blockIdx.x / p.c.kv_heads;
     const int unit = item / p.splits, split = item - unit * p.splits;
 
@@ -985,7 +999,9 @@ struct PrefillPlan {
 // Units at most (rows fill them but for one per sequence), and parts per unit.
 // CTAs run one to an SM, so s parts of c units' tiles take ceil(c s / SMs)
 // turns of tiles / s each, and about four tiles' time for every turn's start,
-// end and joining; from two turns on, parts gain less than they cost.
+// end and joining; from two turns on, parts gain less than they cost. (Two
+// sequences of 512 tokens behind up to 16000, 5 heads of 4: 182, 162, 164, 160, 177, 175, 189, 207 us
+// with 2, 3, 4, 5, 6, 7, 9, 11 parts; 5 are taken.)
 PrefillPlan plan_prefill(const Kv4View &c, int D, int q_heads, int T)
 {
     PrefillPlan d;
