@@ -31,16 +31,20 @@ struct Kv4View {
     }
 };
 
-// The cached length of sequence b that a kernel works with: a negative one is
-// an empty sequence, one beyond the page table is cut to it (and reported).
-__device__ __forceinline__ int kv4_len(const Kv4View &c, const int32_t *lens, int b)
+// The cached length that a kernel works with, of the one given: a negative one
+// is an empty sequence, one beyond the page table is cut to it (and reported).
+__device__ __forceinline__ int kv4_cut(const Kv4View &c, int n)
 {
-    const int n = lens[b];
     if (n > c.max_len()) {
         atomicOr(c.err, kErrBadPage);
         return c.max_len();
     }
     return max(n, 0);
+}
+
+__device__ __forceinline__ int kv4_len(const Kv4View &c, const int32_t *lens, int b)
+{
+    return kv4_cut(c, lens[b]);
 }
 
 }  // namespace tq

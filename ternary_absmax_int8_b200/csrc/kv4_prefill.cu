@@ -68,11 +68,32 @@ struct PrefillShape {
     static constexpr int kPacked = 128 * D / 2;  // a tile's key or value codes
 };
 
+// Division of whole numbers below 2^31 by d: with 2^(l-1) < d <= 2^l and
+// m = ceil(2^(31+l) / d), m d exceeds 2^(31+l) by less than 2^l, so that
+// x m / 2^(31+l) is above x / d by less than 1 / d.
+struct Divisor {
+    unsigned m;
+    int shift;
+
+    Divisor() = default;
+    explicit Divisor(int d) : m(0), shift(31)
+    {
+        while ((1ll << (shift - 31)) < d)
+            ++shift;
+        m = unsigned(((1ull << shift) + unsigned(d) - 1) / unsigned(d));
+    }
+    __device__ __forceinline__ int of(int x) const
+    {
+        return int((unsigned long long)unsigned(x) * m >> shift);
+    }
+};
+
 struct PrefillParams {
     Kv4View c;
     Kv4Query q;
     const int32_t *tok_start, *lens;
     int T, rep, splits;
+    Divisor by_rep, by_heads, by_splits;  // of rep, kv_heads, splits
     float *parts;   // [units][kv_heads][splits][256][D] where splits > 1
     float2 *sums;   // [units][kv_heads][splits][256]: maximum (base 2), sum
 };
@@ -86,30 +107,25 @@ struct Unit {
     int pos0;    // position of its first token
 };
 
-__device__ __forceinline__ int seq_tokens(const PrefillParams &p, int b, int *start)
-{
-    const int s = max(p.tok_start[b], 0), e = min(p.tok_start[b + 1], p.T);
-    *start = s;
-    return max(e - s, 0);
-}
-
-__device__ __forceinline__ int seq_units(const PrefillParams &p, int b)
-{
-    int s;
-    return b < p.c.batch ? (seq_tokens(p, b, &s) * p.rep + kRows - 1) / kRows : 0;
-}
-
 // The sequence that unit `u` counted from the call's last one belongs to: late
 // units of a prompt see most keys, so they start first.
 __device__ Unit find_unit(const PrefillParams &p, int u, int *scratch)
 {
     const int threads = blockDim.x, warps = threads >> 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Unit r{-1, 0, 0, 0, 0};
+    Unit *found = reinterpret_cast<Unit *>(scratch + 32);
     int before = 0;  // units of the sequences behind the present block (from the back)
     for (int b0 = 0; b0 < p.c.batch; b0 += threads) {
         const int b = p.c.batch - 1 - b0 - int(threadIdx.x);
-        const int own = b >= 0 ? seq_units(p, b) : 0;
+        Unit mine{b, 0, 0, 0, 0};
+        int own = 0, end = 0, len = 0;
+        if (b >= 0) {
+            len = p.lens[b];
+            end = p.tok_start[b + 1];
+            mine.start = max(p.tok_start[b], 0);
+            mine.n = max(min(end, p.T) - mine.start, 0);
+            own = (mine.n * p.rep + kRows - 1) / kRows;
+        }
         int incl = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -127,21 +143,15 @@ __device__ Unit find_unit(const PrefillParams &p, int u, int *scratch)
         }
         const int lo = base + incl - own;
         if (u >= lo && u < lo + own) {
-            scratch[32] = b;
-            scratch[33] = own - 1 - (u - lo);
+            mine.row0 = (own - 1 - (u - lo)) * kRows;
+            mine.pos0 = kv4_cut(p.c, len) - (end - mine.start);
+            *found = mine;
         }
         __syncthreads();
-        if (u < before) {
-            r.b = scratch[32];
-            r.row0 = scratch[33] * kRows;
-            break;
-        }
+        if (u < before)
+            return *found;
     }
-    if (r.b >= 0) {
-        r.n = seq_tokens(p, r.b, &r.start);
-        r.pos0 = kv4_len(p.c, p.lens, r.b) - (p.tok_start[r.b + 1] - r.start);
-    }
-    return r;
+    return Unit{-1, 0, 0, 0, 0};
 }
 
 // Key tiles [first, last) of 128 that a unit's split works through.
@@ -153,13 +163,13 @@ struct Tiles {
 __device__ __forceinline__ Tiles tiles_of(const PrefillParams &p, const Unit &u, int split)
 {
     const int last_row = min(u.row0 + kRows, u.n * p.rep) - 1;
-    const int p0 = u.pos0 + u.row0 / p.rep, p1 = u.pos0 + last_row / p.rep;
+    const int p0 = u.pos0 + p.by_rep.of(u.row0), p1 = u.pos0 + p.by_rep.of(last_row);
     Tiles t;
     t.end = min(max(p1 + 1, 0), p.c.max_len());
     t.begin = p.q.window > 0 ? max(0, p0 - p.q.window + 1) : 0;
     const int a = t.begin / kKeys, n = max(0, (t.end + kKeys - 1) / kKeys - a);
-    t.first = a + int((long long)n * split / p.splits);
-    t.last = a + int((long long)n * (split + 1) / p.splits);
+    t.first = a + p.by_splits.of(n * split);  // (at most 2^23 tiles, 32 parts)
+    t.last = a + p.by_splits.of(n * (split + 1));
     return t;
 }
 
@@ -352,7 +362,7 @@ __device__ __forceinline__ uint4 expand_values(uint32_t w)
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t scales[kScaleSlots];
-    uint64_t q_full[2];
+    uint64_t q_raw[8], q_full[2];  // q_raw: of each softmax warp
     uint64_t s_full[2][2], p_full[2][2], o_done[2], o_final[2];  // [row tile][half tile]
     uint64_t packed_full[2][2], packed_empty[2][2];  // [keys, values][stage]
 };
@@ -375,7 +385,7 @@ struct Shared {
     Bars bar;
     __device__ __forceinline__ int *scratch()  // only until the roles part
     {
-        return reinterpret_cast<int *>(v[0]);
+        return reinterpret_cast<int *>(vs[0]);
     }
 };
 
@@ -391,22 +401,119 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     // next to each other: the CTAs that see most keys start first. (With one
     // head's units after the other's, the last head's long ones start when SMs
     // run dry: 422 us instead of 380 for 8192 tokens.)
-    const int kvh = blockIdx.x % p.c.kv_heads, item = blockIdx.x / p.c.kv_heads;
-    const int unit = item / p.splits, split = item - unit * p.splits;
+    const int item = p.by_heads.of(blockIdx.x), kvh = int(blockIdx.x) - item * p.c.kv_heads;
+    const int unit = p.by_splits.of(item), split = item - unit * p.splits;
 
     pdl_wait();
     pdl_launch_dependents();
+    if (warp == 12) {  // (while the others look up lengths)
+        tmem_alloc(&sh.tmem, 512);
+        tc_fence_before();
+    }
     const Unit u = find_unit(p, unit, sh.scratch());
-    if (u.b < 0)
+    if (u.b < 0) {
+        if (warp == 12)
+            tmem_dealloc(sh.tmem, 512);
         return;
+    }
     const Tiles tl = tiles_of(p, u, split);
     const int n = tl.last - tl.first;
     const int rows = min(kRows, u.n * p.rep - u.row0);
     const int nq = rows > 128 ? 2 : 1;  // row tiles at work
+    // The softmax warps' rows, one a thread. A warp's query rows come by bulk
+    // copies, one for each token's heads, into the value tiles, which wait for
+    // them (plain loads took 5000 cycles, longer than the first keys).
+    const int row = threadIdx.x;
+    const int tok = p.by_rep.of(u.row0 + row), h = (u.row0 + row) - tok * p.rep;
+    const bool real = row < rows;
+    const long long row_at = (long long)(kvh * p.rep + h) * D;  // within its token's row
+    const uint8_t *raw = sh.v[0] + row * (2 * D);
+    if (warp < 8 && n > 0 && (warp >> 2) < nq) {
+        uint64_t *bar = &sh.bar.q_raw[warp];
+        if (lane == 0) {
+            mbar_init(bar, 1);
+            fence_mbar_init();
+            mbar_arrive_expect_tx(bar, max(0, min(32, rows - warp * 32)) * uint32_t(2 * D));
+        }
+        __syncwarp();
+        if (real && (h == 0 || lane == 0))
+            bulk_copy(const_cast<uint8_t *>(raw), p.q.q + (u.start + tok) * p.q.q_stride + row_at,
+                      2 * D * min(p.rep - h, min(32 - lane, rows - row)), bar);
+    }
+
+    // Copies of packed codes, by warp 13. Lane 4 g + w: page g of a tile; w: its
+    // key codes, value codes, key scales, value scales.
+    const int copy_g = lane >> 2, copy_w = lane & 3;
+    auto wanted = [&](int tile) {
+        const int index = tile * (kKeys >> p.c.lg_ps) + copy_g;
+        // (a page in front of a window may have gone to another sequence)
+        return copy_g < kKeys >> p.c.lg_ps && index << p.c.lg_ps < tl.end &&
+               (index + 1) << p.c.lg_ps > tl.begin;
+    };
+    auto page_of = [&](int tile) {
+        return wanted(tile) ? p.c.table[(long long)u.b * p.c.max_pages +
+                                        tile * (kKeys >> p.c.lg_ps) + copy_g]
+                            : 0;
+    };
+    int next_page = 0;
+    auto copy_tile = [&](int j) {
+        const int ps = p.c.page_size(), g = copy_g, w = copy_w;
+        const int st = j & 1, parity = ((j >> 1) & 1) ^ 1, page = next_page;
+        if (j + 1 < n)
+            next_page = page_of(tl.first + j + 1);
+        const bool want = wanted(tl.first + j);
+        const bool bad = want && unsigned(page) >= unsigned(p.c.num_pages);
+        const uint32_t there = __ballot_sync(0xffffffffu, want && !bad && w == 0);
+        const uint32_t wrong = __ballot_sync(0xffffffffu, bad && w == 0);
+        const uint8_t *src = p.c.pages + kvh * p.c.template head_bytes<D>() +
+                             (long long)page * p.c.page_stride +
+                             (w < 2 ? (long long)w * ps * (D / 2)
+                                    : (long long)ps * D + (w - 2) * 2 * ps);
+        if (j >= 2 && !mbar_wait_warp(&sh.bar.packed_empty[0][st], parity, p.c.err))
+            return false;
+        if (lane == 0) {
+            uint32_t a = 0, b = 0;  // a bit a page
+            for (int k = 0; k < 8; ++k) {
+                a |= (there >> (4 * k) & 1) << k;
+                b |= (wrong >> (4 * k) & 1) << k;
+            }
+            if (b)
+                atomicOr(p.c.err, kErrBadPage);
+            sh.pages[st] = a | b << 16;
+            mbar_arrive_expect_tx(&sh.bar.packed_full[0][st],
+                                  __popc(there) * uint32_t(ps) * (D / 2 + 4));
+        }
+        __syncwarp();
+        if (want && !bad && w != 1)
+            bulk_copy(w == 0 ? sh.packed[0][st] + g * ps * (D / 2)
+                             : reinterpret_cast<uint8_t *>(&sh.scales[st][w - 2][g * ps]),
+                      src, w == 0 ? ps * (D / 2) : ps * 2, &sh.bar.packed_full[0][st]);
+        if (j >= 2 && !mbar_wait_warp(&sh.bar.packed_empty[1][st], parity, p.c.err))
+            return false;
+        if (lane == 0)
+            mbar_arrive_expect_tx(&sh.bar.packed_full[1][st],
+                                  __popc(there) * uint32_t(ps) * (D / 2));
+        __syncwarp();
+        if (want && !bad && w == 1)
+            bulk_copy(sh.packed[1][st] + g * ps * (D / 2), src, ps * (D / 2),
+                      &sh.bar.packed_full[1][st]);
+        return true;
+    };
 
     if (n > 0) {
-        if (threadIdx.x == 0) {
-            for (int i = 0; i < 2; ++i) {
+        if (warp == 13) {  // the first keys come while all else is set up
+            next_page = page_of(tl.first);
+            if (lane < 4) {
+                mbar_init(&sh.bar.packed_full[lane & 1][lane >> 1], 1);
+                mbar_init(&sh.bar.packed_empty[lane & 1][lane >> 1], 4);
+                fence_mbar_init();
+            }
+            __syncwarp();
+            copy_tile(0);
+        }
+        if (warp == 15) {
+            if (lane < 2) {
+                const int i = lane;
                 mbar_init(&sh.bar.k_full[i], 4);
                 mbar_init(&sh.bar.k_empty[i], nq);
                 mbar_init(&sh.bar.v_full[i], 4);
@@ -418,18 +525,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                 mbar_init(&sh.bar.o_done[i], 1);
                 mbar_init(&sh.bar.o_final[i], 1);
                 mbar_init(&sh.bar.q_full[i], 4);
-                for (int w = 0; w < 2; ++w) {
-                    mbar_init(&sh.bar.packed_full[w][i], 1);
-                    mbar_init(&sh.bar.packed_empty[w][i], 4);
-                }
             }
-            for (int i = 0; i < kScaleSlots; ++i)
-                mbar_init(&sh.bar.scales[i], 4);
+            if (lane < kScaleSlots)
+                mbar_init(&sh.bar.scales[lane], 4);
             fence_mbar_init();
         }
-        if (warp == 12)
-            tmem_alloc(&sh.tmem, 512);
-        tc_fence_before();
         __syncthreads();
         tc_fence_after();
     }
@@ -438,71 +538,60 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     if (warp < 8) {
         // ---------------------------------------------------------- softmax
         const int s = warp >> 2;
-        const int row = s * 128 + (warp & 3) * 32 + lane;
-        const int tok = (u.row0 + row) / p.rep, h = (u.row0 + row) - tok * p.rep;
-        const bool real = row < rows;
         const int pos = real ? u.pos0 + tok : -1;
         const int low = p.q.window > 0 ? pos - p.q.window + 1 : 0;  // first key seen
         // what all rows of the tile see: keys [low_max, pos_min]
-        const int pos_min = u.pos0 + (u.row0 + s * 128) / p.rep;
+        const int pos_min = u.pos0 + p.by_rep.of(u.row0 + s * 128);
         const int last = min(s * 128 + 127, rows - 1);
         const int low_max =
-            p.q.window > 0 ? u.pos0 + (u.row0 + last) / p.rep - p.q.window + 1 : 0;
+            p.q.window > 0 ? u.pos0 + p.by_rep.of(u.row0 + last) - p.q.window + 1 : 0;
         const uint32_t lane_at = uint32_t((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_at + s * 128, to = tmem + lane_at + 256 + s * D;
-        const long long row_at = (long long)(kvh * p.rep + h) * D;  // within its token's row
-        // The warp's query rows, D/8 lanes a row, all loads at once (while the
-        // first keys are fetched and expanded), then fp16 against each row's
-        // largest magnitude.
+        // The thread's query row as fp16 against its largest magnitude: 16 bytes at
+        // a time in an order (c = k ^ twist) in which neither the reads nor the
+        // swizzled writes of eight lanes meet in a bank: twist, and twist ^ lane,
+        // take all values of three bits.
         float row_mul = 0.0f;  // what 1 in the row stands for x scale, base 2
+        bool fine = s < nq;
         if (n > 0 && s < nq) {
-            constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks, kTimes = kChunks;
-            const int c = lane % kChunks;
-            const unsigned long long src = reinterpret_cast<unsigned long long>(
-                real ? p.q.q + (u.start + tok) * p.q.q_stride + row_at : nullptr);
-            uint4 v[kTimes];
-#pragma unroll
-            for (int i = 0; i < kTimes; ++i) {
-                const uint4 *from = reinterpret_cast<const uint4 *>(
-                    __shfl_sync(0xffffffffu, src, i * kAtOnce + lane / kChunks));
-                v[i] = from ? __ldg(from + c) : make_uint4(0, 0, 0, 0);
+            const int twist = ((lane << 1) & 7) ^ ((lane & 4) ? 3 : 0);
+            fine = mbar_wait_warp(&sh.bar.q_raw[warp], 0, p.c.err);
+            auto chunk = [&](int c) {
+                return real ? lds128(raw + (c << 4)) : make_uint4(0, 0, 0, 0);
+            };
+            uint32_t tops = 0;
+#pragma unroll 4
+            for (int k = 0; k < D / 8; ++k) {
+                const uint4 x = chunk(k ^ twist);
+                tops = __vmaxu2(tops, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                               __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
             }
-            uint32_t mine = 0;  // largest magnitude of the thread's own row, fp32 bits
-#pragma unroll
-            for (int i = 0; i < kTimes; ++i) {
-                uint32_t top = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
-                                        __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
-                top = max(top & 0xFFFFu, top >> 16) << 16;
-#pragma unroll
-                for (int o = kChunks / 2; o > 0; o >>= 1)
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const uint32_t its = __shfl_sync(0xffffffffu, top, (lane % kAtOnce) * kChunks);
-                if (lane / kAtOnce == i)
-                    mine = its;
-                const float down = __uint_as_float(uint32_t(127 - row_exponent(top)) << 23);
-                const float f[8] = {bf16_lo(v[i].x), bf16_hi(v[i].x), bf16_lo(v[i].y),
-                                    bf16_hi(v[i].y), bf16_lo(v[i].z), bf16_hi(v[i].z),
-                                    bf16_lo(v[i].w), bf16_hi(v[i].w)};
+            const uint32_t top = max(tops & 0xFFFFu, tops >> 16) << 16;  // fp32 bits
+            const float down = __uint_as_float(uint32_t(127 - row_exponent(top)) << 23);
+#pragma unroll 4
+            for (int k = 0; k < D / 8; ++k) {
+                const int c = k ^ twist;
+                const uint4 x = chunk(c);
+                const float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
+                                    bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const __half2 x = __floats2half2_rn(f[e] * down, f[4 + e] * down);
-                    w[e] = *reinterpret_cast<const uint32_t *>(&x);
+                    const __half2 y = __floats2half2_rn(f[e] * down, f[4 + e] * down);
+                    w[e] = *reinterpret_cast<const uint32_t *>(&y);
                 }
-                *reinterpret_cast<uint4 *>(
-                    sh.q[s] + (c >> 3) * 16384 +
-                    sw128_off((warp & 3) * 32 + i * kAtOnce + lane / kChunks, c & 7)) =
+                *reinterpret_cast<uint4 *>(sh.q[s] + (c >> 3) * 16384 +
+                                           sw128_off(row & 127, c & 7)) =
                     make_uint4(w[0], w[1], w[2], w[3]);
             }
-            row_mul = mine >= 0x7F800000u
-                          ? NAN
-                          : __uint_as_float(uint32_t(127 + row_exponent(mine)) << 23) *
-                                (p.q.scale * kLog2e);
+            row_mul = top >= 0x7F800000u ? NAN
+                                         : __uint_as_float(uint32_t(127 + row_exponent(top)) << 23) *
+                                               (p.q.scale * kLog2e);
             fence_proxy_async_smem();
             warp_arrive(&sh.bar.q_full[s]);
         }
         float m = -INFINITY, lsum = 0.0f;  // m: base 2, of scale x scores
-        bool poisoned = false, fine = s < nq;
+        bool poisoned = false;
 #pragma unroll 1
         for (int i = 0; i < 2 * n && fine; ++i) {  // half tiles
             const int slot = (i >> 1) % kScaleSlots, half = i & 1;
@@ -608,10 +697,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             warp_arrive(&sh.bar.p_full[s][half]);
         }
         // Output rows (a row tile without keys, or without rows, has none).
-        if (n > 0 && s < nq) {
-            fine = fine && mbar_wait_warp(&sh.bar.o_final[s], 0, p.c.err);
-            tc_fence_after();
-        }
         const float inv = lsum == 0.0f ? 0.0f : poisoned ? NAN : 1.0f / lsum;
         const long long token = u.start + tok;
         const long long part = ((((long long)unit * p.c.kv_heads + kvh) * p.splits + split) *
@@ -623,10 +708,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             constexpr int kChunks = D / 8;  // of 16 bytes
             uint8_t *stage = sh.q[s] + (warp & 3) * 32 * (2 * D);
             const bool parts = p.splits > 1;
+            const float by = !parts || lsum == 0.0f ? inv : poisoned ? NAN : 1.0f;
             char *dst = parts ? reinterpret_cast<char *>(p.parts + part * D)
                               : reinterpret_cast<char *>(p.q.out + token * p.q.out_stride + row_at);
             if (!real)
                 dst = nullptr;
+            if (n > 0) {
+                fine = fine && mbar_wait_warp(&sh.bar.o_final[s], 0, p.c.err);
+                tc_fence_after();
+            }
             auto put = [&](int chunk, uint4 v) {
                 *reinterpret_cast<uint4 *>(stage + lane * 2 * D + ((chunk ^ (lane & 7)) << 4)) = v;
             };
@@ -663,10 +753,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                         e[k] = __uint_as_float(o[8 * c + 2 * k]);
                         e[4 + k] = __uint_as_float(o[8 * c + 2 * k + 1]);
                     }
-                    const float by = parts ? poisoned ? NAN : 1.0f : inv;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        e[k] = lsum == 0.0f ? 0.0f : e[k] * by;
+                        e[k] *= by;
                     if (parts) {
                         const int at = (32 * i) % (D / 2) / 4 + 2 * c;
                         put(at, make_uint4(__float_as_uint(e[0]), __float_as_uint(e[1]),
@@ -778,6 +867,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                    mbar_wait_warp(&sh.bar.packed_full[1][st], parity, p.c.err);
             if (!fine)
                 break;
+            if (j == 0)  // the query rows lie there until they are converted
+                for (int s = 0; s < nq; ++s)
+                    fine = fine && mbar_wait_warp(&sh.bar.q_full[s], 0, p.c.err);
+            if (!fine)
+                break;
             expand(sh.v[st], sh.packed[1][st], false, scale);
             fence_proxy_async_smem();
             warp_arrive(&sh.bar.v_full[st]);
@@ -868,71 +962,16 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         }
         // ------------------------------------------------------------ copies
         if (warp == 13) {
-            // Lane 4 g + w: page g of a tile; w: its key codes, value codes, key
-            // scales, value scales.
-            const int ps = p.c.page_size(), per_tile = kKeys >> p.c.lg_ps;
-            const int g = lane >> 2, w = lane & 3;
-            const int32_t *table = p.c.table + (long long)u.b * p.c.max_pages;
-            const uint8_t *head = p.c.pages + kvh * p.c.template head_bytes<D>();
-            const long long off = w < 2 ? (long long)w * ps * (D / 2)
-                                        : (long long)ps * D + (w - 2) * 2 * ps;
-            auto wanted = [&](int tile) {
-                const int index = tile * per_tile + g;
-                // (a page in front of a window may have gone to another sequence)
-                return g < per_tile && index << p.c.lg_ps < tl.end &&
-                       (index + 1) << p.c.lg_ps > tl.begin;
-            };
-            auto page_of = [&](int tile) { return wanted(tile) ? table[tile * per_tile + g] : 0; };
-            int next = n > 0 ? page_of(tl.first) : 0;
-            bool fine = true;
 #pragma unroll 1
-            for (int j = 0; j < n; ++j) {
-                const int st = j & 1, parity = ((j >> 1) & 1) ^ 1, page = next;
-                if (j + 1 < n)
-                    next = page_of(tl.first + j + 1);
-                const bool want = wanted(tl.first + j);
-                const bool bad = want && unsigned(page) >= unsigned(p.c.num_pages);
-                const uint32_t there = __ballot_sync(0xffffffffu, want && !bad && w == 0);
-                const uint32_t wrong = __ballot_sync(0xffffffffu, bad && w == 0);
-                const uint8_t *src = head + (long long)page * p.c.page_stride + off;
-                fine = (j < 2 || mbar_wait_warp(&sh.bar.packed_empty[0][st], parity, p.c.err));
-                if (!fine)
-                    break;
-                if (lane == 0) {
-                    uint32_t a = 0, b = 0;  // a bit a page
-                    for (int k = 0; k < 8; ++k) {
-                        a |= (there >> (4 * k) & 1) << k;
-                        b |= (wrong >> (4 * k) & 1) << k;
-                    }
-                    if (b)
-                        atomicOr(p.c.err, kErrBadPage);
-                    sh.pages[st] = a | b << 16;
-                    mbar_arrive_expect_tx(&sh.bar.packed_full[0][st],
-                                          __popc(there) * uint32_t(ps) * (D / 2 + 4));
-                }
-                __syncwarp();
-                if (want && !bad && w != 1)
-                    bulk_copy(w == 0 ? sh.packed[0][st] + g * ps * (D / 2)
-                                    : reinterpret_cast<uint8_t *>(&sh.scales[st][w - 2][g * ps]),
-                             src, w == 0 ? ps * (D / 2) : ps * 2, &sh.bar.packed_full[0][st]);
-                fine = (j < 2 || mbar_wait_warp(&sh.bar.packed_empty[1][st], parity, p.c.err));
-                if (!fine)
-                    break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&sh.bar.packed_full[1][st],
-                                          __popc(there) * uint32_t(ps) * (D / 2));
-                __syncwarp();
-                if (want && !bad && w == 1)
-                    bulk_copy(sh.packed[1][st] + g * ps * (D / 2), src, ps * (D / 2),
-                              &sh.bar.packed_full[1][st]);
-            }
+            for (int j = 1; j < n && copy_tile(j); ++j)
+                ;
         }
         __syncwarp();
     }
     __syncthreads();
-    if (warp == 12 && n > 0) {
+    if (warp == 12) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(sh.tmem, 512);
     }
 }
 
@@ -943,7 +982,7 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
     kv4_prefill_join_kernel(const __grid_constant__ PrefillParams p)
 {
-    __shared__ int scratch[34];
+    __shared__ int scratch[40];
     pdl_wait();
     pdl_launch_dependents();
     const Unit u = find_unit(p, blockIdx.x, scratch);
@@ -978,7 +1017,7 @@ __global__ void __launch_bounds__(kJoinThreads)
                 v[i].y = fmaf(wk, x.y, v[i].y);
             }
         }
-        const int tok = (u.row0 + r) / p.rep, h = (u.row0 + r) - tok * p.rep;
+        const int tok = p.by_rep.of(u.row0 + r), h = (u.row0 + r) - tok * p.rep;
         const long long token = u.start + tok;
         const int head = kvh * p.rep + h;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -1085,6 +1124,9 @@ cudaError_t launch_kv4_prefill(const Kv4View &c, int D, const Kv4Query &q,
     p.T = T;
     p.rep = plan.rep;
     p.splits = plan.splits;
+    p.by_rep = Divisor(plan.rep);
+    p.by_heads = Divisor(c.kv_heads);
+    p.by_splits = Divisor(plan.splits);
     p.parts = static_cast<float *>(workspace);
     p.sums = reinterpret_cast<float2 *>(p.parts + size_t(plan.units) * c.kv_heads * plan.splits *
                                                       kRows * size_t(D));
