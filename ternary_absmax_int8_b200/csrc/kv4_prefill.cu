@@ -29,17 +29,21 @@
 // tensor core needs 4 x 512 cycles, the 2 x 16384 exponentials 2048 at 16 a
 // cycle, shared memory about 2300 (operands 1536, expanded codes 512, scales
 // 256), all instructions about 2600 issue slots of each scheduler; but a pair of
-// tiles takes 4800, as the two softmax warps of a scheduler do not cover the
+// tiles takes 4200, as the two softmax warps of a scheduler do not cover the
 // latencies of their own chain (scores from tensor memory, maximum, exponentials,
-// weights back), and a CTA's start and end take 17000 together. A prompt of 8192
-// tokens (20 heads on 5, D = 128; 344 GFLOP) takes 380 us, 905 TFLOP/s, 55% of a
-// plain library product's rate (tensor pipe 39% busy, issue slots 51%, exponentials
-// 41% over 4096 tokens). What was tried, in us for that prompt: scores of whole
-// tiles, not ahead 519, of half tiles two ahead 422 (380 with all heads' long
-// units first); four softmax warpgroups 490 where two took 449; the next scores
-// fetched before the exponentials 534 then (spills); registers dealt anew between
-// the roles 386; the row tiles' softmax taking turns 394; a part of the
-// exponentials as polynomials 387 and more; waits that sleep longer 395.
+// weights back). A CTA's start takes 9000 cycles (lengths, keys and queries from
+// memory, their expansion), its end 4500, the next CTA's arrival 1900. A prompt of
+// 8192 tokens (20 heads on 5, D = 128; 344 GFLOP) takes 367 us, 937 TFLOP/s, 57%
+// of a plain library product's rate (tensor pipe 39% busy, issue slots 51%,
+// exponentials 41% over 4096 tokens). What was tried, in us for that prompt:
+// scores of whole tiles, not ahead 519, of half tiles two ahead 422 (380 with all
+// heads' long units first, 367 with the shorter start); four softmax warpgroups
+// 490 where two took 449; the next scores fetched before the exponentials 534
+// then (spills). Where 380 was the measure: registers dealt anew between the
+// roles 386; the row tiles' softmax taking turns 394; a part of the exponentials
+// as polynomials 387 and more; waits that sleep longer 395. Where 367 was: the
+// next scores asked for before the weights' arrival is awaited, with the weights
+// handed on then 375, in time 412 (spills).
 //
 // Few rows over a long cache are split along the keys, into parts that
 // kv4_prefill_join_kernel adds up in order.
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     // Units are counted from the call's last row, and their heads and parts stand
     // next to each other: the CTAs that see most keys start first. (With one
     // head's units after the other's, the last head's long ones start when SMs
-    // run dry: 422 us instead of 380 for 8192 tokens.)
+    // run dry: 422 us for 8192 tokens where this order took 380.)
     const int item = p.by_heads.of(blockIdx.x), kvh = int(blockIdx.x) - item * p.c.kv_heads;
     const int unit = p.by_splits.of(item), split = item - unit * p.splits;
 
@@ -559,19 +563,23 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             auto chunk = [&](int c) {
                 return real ? lds128(raw + (c << 4)) : make_uint4(0, 0, 0, 0);
             };
+            uint4 v[D / 8];
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k)
+                v[k] = chunk(k ^ twist);
             uint32_t tops = 0;
-#pragma unroll 4
+#pragma unroll
             for (int k = 0; k < D / 8; ++k) {
-                const uint4 x = chunk(k ^ twist);
+                const uint4 x = v[k];
                 tops = __vmaxu2(tops, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
                                                __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
             }
             const uint32_t top = max(tops & 0xFFFFu, tops >> 16) << 16;  // fp32 bits
             const float down = __uint_as_float(uint32_t(127 - row_exponent(top)) << 23);
-#pragma unroll 4
+#pragma unroll
             for (int k = 0; k < D / 8; ++k) {
                 const int c = k ^ twist;
-                const uint4 x = chunk(c);
+                const uint4 x = v[k];
                 const float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
                                     bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
                 uint32_t w[4];
@@ -1040,7 +1048,7 @@ struct PrefillPlan {
 // turns of tiles / s each, and about four tiles' time for every turn's start,
 // end and joining; from two turns on, parts gain less than they cost. (Two
 // sequences of 512 tokens behind up to 16000, 5 heads of 4: 182, 162, 164, 160, 177, 175, 189, 207 us
-// with 2, 3, 4, 5, 6, 7, 9, 11 parts; 5 are taken.)
+// with 2, 3, 4, 5, 6, 7, 9, 11 parts when 5 parts took 160; they take 152.5 now.)
 PrefillPlan plan_prefill(const Kv4View &c, int D, int q_heads, int T)
 {
     PrefillPlan d;
