@@ -12,9 +12,10 @@
 // group of D/8 lanes holds one (token, head) pair of rows, 8 values of each
 // per lane with 16-byte loads, and the largest magnitude is a shuffle
 // reduction inside the group. Prompts of 13,400 tokens in all, 5 heads of
-// 128 in fp32 (77 MB), take 18.3 us, 4.2 TB/s: instructions are as near a bound
-// (issue slots 65% busy). One round of items per CTA, instead of several with the
-// next rows fetched ahead: 21.6 us.
+// 128 in fp32 (77 MB), take 16.3 us, 4.7 TB/s: instructions are as near a bound
+// (issue slots 65% busy at 18.3 us, when whole rounds per CTA left some SMs short).
+#include <algorithm>
+
 #include "kv4_common.cuh"
 #include "quant_core.cuh"
 
@@ -23,6 +24,7 @@ namespace tq {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr int kLoopCtas = 3, kOnceCtas = 4;  // of an SM
 
 struct AppendParams {
     Kv4View c;
@@ -31,7 +33,7 @@ struct AppendParams {
     unsigned k_stride, v_stride, page_stride;
     const int32_t *tok_start, *lens;
     int T, items;  // items: (token, head) pairs
-    int per_cta;   // of them, a multiple of the CTA's groups
+    int each, more;  // rounds (an item of each group) of a CTA: the first `more` have each + 1
 };
 
 // Eight codes + 8, four bits each, first value lowest: the whole numbers
@@ -145,18 +147,21 @@ __device__ __forceinline__ void put_row(const float (&x)[8], uint32_t sbits, flo
     }
 }
 
-template <int D, bool F32>
-__global__ void __launch_bounds__(kAppendThreads, 4)
+// kLoop: a CTA's items go round; else each group has one.
+template <int D, bool F32, bool kLoop>
+__global__ void __launch_bounds__(kAppendThreads, kLoop ? kLoopCtas : kOnceCtas)
     kv4_append_kernel(const __grid_constant__ AppendParams p)
 {
     constexpr int kLanes = D / 8, kGroups = kAppendThreads / kLanes;
     const int lane = threadIdx.x % kLanes;
     pdl_wait();
     pdl_launch_dependents();
-    // A CTA's items are consecutive (token, head) pairs, kGroups at a time; the
-    // next ones' rows are on their way while the present ones are quantised.
-    const int start = blockIdx.x * p.per_cta, first = start + threadIdx.x / kLanes;
-    const int stop = min(p.items - start, p.per_cta) + start;
+    // A CTA's items are consecutive (token, head) pairs, kGroups at a time; where
+    // it goes round, the next ones' rows are on their way while the present ones
+    // are quantised.
+    const int cta = blockIdx.x, round0 = cta * p.each + min(cta, p.more);
+    const int first = round0 * kGroups + threadIdx.x / kLanes;
+    const int stop = min(p.items, (round0 + p.each + (cta < p.more)) * kGroups);
     float k[8], v[8], next_k[8], next_v[8];
     int t = first / p.c.kv_heads, h = first - t * p.c.kv_heads;
     auto load = [&](bool real, int at, int head, float (&kk)[8], float (&vv)[8]) {
@@ -206,13 +211,14 @@ __global__ void __launch_bounds__(kAppendThreads, 4)
     int page = 0, at = locate(first < stop, t, &page);
     // (a warp's groups go round together: lanes without a row stay for the
     // shuffles and store nothing)
+#pragma unroll 2
     for (int item = first; item - int(threadIdx.x / kLanes) < stop; item += kGroups) {
         int next_t = t, next_h = h + kGroups, next_page = 0;
         while (next_h >= p.c.kv_heads) {
             next_h -= p.c.kv_heads;
             ++next_t;
         }
-        const bool more = stop - item > kGroups;
+        const bool more = kLoop && stop - item > kGroups;
         load(more, next_t, next_h, next_k, next_v);
         const int next_at = locate(more, next_t, &next_page);
 
@@ -247,6 +253,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4)
         put_row<D>(v, __shfl_sync(0xffffffffu, sbits, even + 1),
                    __shfl_sync(0xffffffffu, inv, even + 1), lane, codes + ps * (D / 2), scale + ps,
                    store);
+        if (!kLoop)
+            break;
         t = next_t;
         h = next_h;
         at = next_at;
@@ -259,6 +267,15 @@ __global__ void __launch_bounds__(kAppendThreads, 4)
     }
 }
 
+template <int D>
+cudaError_t launch(const cudaLaunchConfig_t *cfg, bool f32, bool loop, const AppendParams &p)
+{
+    if (!f32)
+        return cudaLaunchKernelEx(cfg, kv4_append_kernel<D, false, false>, p);
+    return loop ? cudaLaunchKernelEx(cfg, kv4_append_kernel<D, true, true>, p)
+                : cudaLaunchKernelEx(cfg, kv4_append_kernel<D, true, false>, p);
+}
+
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4View &c, int D, const void *k, const void *v, bool f32,
@@ -267,13 +284,17 @@ cudaError_t launch_kv4_append(const Kv4View &c, int D, const void *k, const void
 {
     const long long items = (long long)T * c.kv_heads;
     const int groups = kAppendThreads / (D / 8);
-    // Four CTAs fit an SM; more items than that many groups go round.
-    const long long rounds = (items + groups - 1) / groups;  // of one CTA
-    const long long most = 4ll * device_sm_count();
-    const long long per = rounds <= most ? 1 : (rounds + most - 1) / most;
+    // A round is an item for each group of a CTA. Each CTA has one, so that small
+    // calls spread over all SMs; fp32 rows beyond 16 rounds an SM go round in 3
+    // CTAs per SM, the next ones' loads in flight, as there bytes count more than
+    // instructions. fp32, heads of 128, in us, one round : going round, at 7, 12,
+    // 16, 20, 24 and 40 rounds an SM: 5.1:5.5, 7.2:7.5, 9.7:9.9, 13.2:12.6,
+    // 16.0:14.5, 24.4:21.7; bf16 at 7, 16, 40: 5.5:6.5, 10.2:11.2, 24.8:29.1.
+    const int rounds = int((items + groups - 1) / groups);  // of one CTA
+    const bool loop = f32 && rounds > 16 * device_sm_count();
+    const int grid = loop ? std::min(rounds, kLoopCtas * device_sm_count()) : rounds;
     const AppendParams p{c, k, v, unsigned(k_stride), unsigned(v_stride), unsigned(c.page_stride),
-                         tok_start, lens, T, int(items), int(per) * groups};
-    const long long grid = (rounds + per - 1) / per;
+                         tok_start, lens, T, int(items), rounds / grid, rounds % grid};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid));
     cfg.blockDim = dim3(kAppendThreads);
@@ -283,11 +304,7 @@ cudaError_t launch_kv4_append(const Kv4View &c, int D, const void *k, const void
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (D == 128)
-        return f32 ? cudaLaunchKernelEx(&cfg, kv4_append_kernel<128, true>, p)
-                   : cudaLaunchKernelEx(&cfg, kv4_append_kernel<128, false>, p);
-    return f32 ? cudaLaunchKernelEx(&cfg, kv4_append_kernel<64, true>, p)
-               : cudaLaunchKernelEx(&cfg, kv4_append_kernel<64, false>, p);
+    return D == 128 ? launch<128>(&cfg, f32, loop, p) : launch<64>(&cfg, f32, loop, p);
 }
 
 }  // namespace tq

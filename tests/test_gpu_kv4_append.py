@@ -168,19 +168,21 @@ def test_append_far_pages(cuda_device):
     assert np.array_equal(keep[0][lead:].cpu().numpy(), cache.bytes())
 
 
-def test_append_of_many_sequences(cuda_device):
+@pytest.mark.parametrize("D,hk,f32,batch", [(64, 9, False, 700), (128, 45, True, 100),
+                                            (64, 80, True, 100)])
+def test_append_of_many_sequences(cuda_device, D, hk, f32, batch):
     """More (token, head) pairs than the GPU takes at once, sequences of 0 to 3
     tokens and one long one, tokens beyond tok_start's end ignored."""
     rng = np.random.default_rng(21)
-    n = rng.integers(0, 4, 700)
+    n = rng.integers(0, 4, batch)
     n[::5] = 0
-    n[300] = 900
-    lens = n + rng.integers(0, 20, 700)
-    cache = Cache(rng, lens.tolist(), 9, 64, 16)
+    n[60] = 900
+    lens = n + rng.integers(0, 20, batch)
+    cache = Cache(rng, lens.tolist(), hk, D, 16)
     c, keep = cache.on_gpu()
     T = int(n.sum()) + 5
-    k, v = rows(rng, T, 9, 64, False), rows(rng, T, 9, 64, False)
-    append(c, keep, k, v, False, n.tolist(), lens.tolist())
+    k, v = rows(rng, T, hk, D, f32), rows(rng, T, hk, D, f32)
+    append(c, keep, k, v, f32, n.tolist(), lens.tolist())
     put(cache, k, v, n, lens)
     assert np.array_equal(keep[0].cpu().numpy(), cache.bytes())
     assert tq.tq_device_error() == 0
