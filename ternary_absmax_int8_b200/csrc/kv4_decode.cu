@@ -41,7 +41,7 @@
 // sequence, in a fixed order.
 //
 // Measured (20 heads on 5 of 128, pages of 64): one sequence of 777 tokens
-// 7.2 us; 24 of up to 8191 (65 MB) 22.8 us, 2.8 TB/s; one of 262143 (173 MB)
+// 7.2 us; 24 of up to 8191 (65 MB) 22.2 us, 2.9 TB/s; one of 262143 (173 MB)
 // 38.5 us, 4.5 TB/s. Of the long call the start (lengths, page numbers, first
 // copies) takes 2.7 us, merge and join 4; between them it runs at 6 TB/s with
 // the issue slots 57%, ALUs 53% and matrix pipes 28% busy. The batch's tiles are
@@ -651,6 +651,7 @@ struct Crossing {
 struct Segment {  // a warp's last stretch, for the merge within the CTA
     int item;         // -1: none
     int first, last;  // the item's tiles [first, last) among all
+    int b, head0, heads;  // its sequence and query heads
 };
 
 template <int D, int HG>
@@ -793,7 +794,7 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
     Running<D, HG> run;
     Queries<D, HG> qs;
     bool fine = true;
-    Segment last{-1, 0, 0};
+    Segment last{-1, 0, 0, 0, 0, 0};
     Crossing cross{-1, 0, 0, 0};
     int end_item = -1;
     while (at < stop && fine) {
@@ -915,7 +916,7 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
                               min(p.rows, heads));
             end_item = b * hg + ig;
         } else {
-            last = Segment{b * hg + ig, item0, item0 + sp.tiles};
+            last = Segment{b * hg + ig, item0, item0 + sp.tiles, b, head0, heads};
         }
     }
 
@@ -958,10 +959,8 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
         const Segment sg = seg[w];
         const int n = __popc(__ballot_sync(0xffffffffu, item_w == sg.item));
         const int h = task / (D / 64), d = (task % (D / 64)) * 64 + 2 * lane;
-        const int sb = sg.item / hg, ig = sg.item - sb * hg;
-        const int kvh = ig / p.groups, grp = ig - kvh * p.groups;
         task += S::kWarps;
-        if (h >= min(S::kHeads, p.rep - grp * S::kHeads))
+        if (h >= sg.heads)
             continue;
         const bool more = w + n < S::kWarps && ended[w + n] == sg.item;
         const int from = cta_first + warps.first(w), to = cta_first + warps.first(w + n);
@@ -970,39 +969,31 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
             reinterpret_cast<const float *>(smem) + (w * S::kHeads + h) * S::kPartFloats;
         const float *tail =
             p.parts + ((long long)(2 * (blockIdx.x * S::kWarps + w + n)) * p.rows + h) * (D + 2);
-        // lane k: part k's maximum and sum
-        float2 ml = make_float2(-INFINITY, 0.0f), x_tail = make_float2(0.0f, 0.0f);
-        if (lane < n)
-            ml = *reinterpret_cast<const float2 *>(first + lane * (S::kHeads * S::kPartFloats) + D);
-        else if (more && lane == n)
-            ml = *reinterpret_cast<const float2 *>(tail + D);
-        if (more)
+        float2 ml_tail = make_float2(-INFINITY, 0.0f), x_tail = make_float2(0.0f, 0.0f);
+        if (more) {  // from L2, while the others are added up
+            ml_tail = *reinterpret_cast<const float2 *>(tail + D);
             x_tail = *reinterpret_cast<const float2 *>(tail + d);
+        }
         Joined r;
-        r.m = ml.x;
+        float2 ml[S::kWarps];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            r.m = fmaxf(r.m, __shfl_xor_sync(0xffffffffu, r.m, o));
-        const float wk = ml.x == -INFINITY ? 0.0f : ex2(ml.x - r.m);
-        r.l = wk * ml.y;
+        for (int k = 0; k < S::kWarps; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.0f);
+            if (k < n)
+                ml[k] = *reinterpret_cast<const float2 *>(
+                    first + k * (S::kHeads * S::kPartFloats) + D);
+            r.m = fmaxf(r.m, ml[k].x);
+        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            r.l += __shfl_xor_sync(0xffffffffu, r.l, o);
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float2 x = *reinterpret_cast<const float2 *>(
-                first + k * (S::kHeads * S::kPartFloats) + d);
-            const float f = __shfl_sync(0xffffffffu, wk, k);
-            r.v.x = fmaf(f, x.x, r.v.x);
-            r.v.y = fmaf(f, x.y, r.v.y);
-        }
-        if (more) {
-            const float f = __shfl_sync(0xffffffffu, wk, n);
-            r.v.x = fmaf(f, x_tail.x, r.v.x);
-            r.v.y = fmaf(f, x_tail.y, r.v.y);
-        }
+        for (int k = 0; k < S::kWarps; ++k)
+            if (k < n)
+                r.add_below(*reinterpret_cast<const float2 *>(
+                                first + k * (S::kHeads * S::kPartFloats) + d),
+                            ml[k]);
+        if (more)
+            r.add(x_tail, ml_tail);
         if (whole) {
-            store_joined<D>(p, r, sb, kvh * p.rep + grp * S::kHeads + h, d);
+            store_joined<D>(p, r, sg.b, sg.head0 + h, d);
         } else {
             float *dst =
                 p.parts + ((long long)(2 * (blockIdx.x * S::kWarps + w) + 1) * p.rows + h) * (D + 2);
