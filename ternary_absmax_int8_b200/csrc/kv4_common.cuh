@@ -31,6 +31,26 @@ struct Kv4View {
     }
 };
 
+// Division of whole numbers below 2^31 by d: with 2^(l-1) < d <= 2^l and
+// m = ceil(2^(31+l) / d), m d exceeds 2^(31+l) by less than 2^l, so that
+// x m / 2^(31+l) is above x / d by less than 1 / d.
+struct Divisor {
+    unsigned m;
+    int shift;
+
+    Divisor() = default;
+    explicit Divisor(int d) : m(0), shift(31)
+    {
+        while ((1ll << (shift - 31)) < d)
+            ++shift;
+        m = unsigned(((1ull << shift) + unsigned(d) - 1) / unsigned(d));
+    }
+    __device__ __forceinline__ int of(int x) const
+    {
+        return int((unsigned long long)unsigned(x) * m >> shift);
+    }
+};
+
 // The cached length that a kernel works with, of the one given: a negative one
 // is an empty sequence, one beyond the page table is cut to it (and reported).
 __device__ __forceinline__ int kv4_cut(const Kv4View &c, int n)

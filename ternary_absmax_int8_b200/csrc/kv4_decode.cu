@@ -41,8 +41,8 @@
 // sequence, in a fixed order.
 //
 // Measured (20 heads on 5 of 128, pages of 64): one sequence of 777 tokens
-// 7.2 us; 24 of up to 8191 (65 MB) 22.2 us, 2.9 TB/s; one of 262143 (173 MB)
-// 38.5 us, 4.5 TB/s. Of the long call the start (lengths, page numbers, first
+// 6.7 us; 24 of up to 8191 (65 MB) 22.0 us, 2.9 TB/s; one of 262143 (173 MB)
+// 38.2 us, 4.5 TB/s. Of the long call the start (lengths, page numbers, first
 // copies) takes 2.7 us, merge and join 4; between them it runs at 6 TB/s with
 // the issue slots 57%, ALUs 53% and matrix pipes 28% busy. The batch's tiles are
 // a third of that, and its start and end, with more joins, the same.
@@ -85,6 +85,7 @@ struct DecodeParams {
     int rep;     // query heads per key/value head
     int groups;  // items per key/value head: of up to 4 HG query heads each
     int rows;    // heads of a part: min(rep, 4 HG)
+    Divisor by_groups, by_ctas;
     // workspace
     Crossing *crossing;  // [CTAs]
     float *parts;               // [warps of all CTAs][2][rows][D + 2]
@@ -116,6 +117,10 @@ struct Shares {
     int each, more;
 
     __device__ __forceinline__ Shares(int count, int n) : each(count / n), more(count - each * n) {}
+    __device__ __forceinline__ Shares(int count, int n, const Divisor &by_n)
+        : each(by_n.of(count)), more(count - each * n)
+    {
+    }
     __device__ __forceinline__ int first(int i) const { return i * each + min(i, more); }
     __device__ __forceinline__ int of(int tile) const  // the share that holds tile
     {
@@ -641,8 +646,9 @@ __device__ __forceinline__ void store_joined(const DecodeParams &p, const Joined
 
 // The item that a CTA's share begins in, where it began in an earlier CTA: the
 // combine kernel's work list.
-struct Crossing {
-    int item;    // -1: none, or one that began further back than the CTA before
+struct alignas(8) Crossing {
+    int b;       // its sequence; -1: none, or one that began further back than the CTA before
+    int head0, heads;  // its query heads
     int parts;   // CTAs that hold a part of it, from the one before on
     int warp0;   // the warp that it begins in there
     int ended;   // its last part is in that CTA's first warp's slot 0
@@ -717,7 +723,7 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
             empty_rows(lane, own);
         const int incl = running_sum(own);
         total = __shfl_sync(0xffffffffu, incl, 31);
-        const Shares ctas(total, gridDim.x);
+        const Shares ctas(total, gridDim.x, p.by_ctas);
         cta_first = ctas.first(blockIdx.x);
         cta_stop = ctas.first(blockIdx.x + 1);
         const int at = cta_first + Shares(cta_stop - cta_first, S::kWarps).first(warp);
@@ -746,7 +752,7 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
             base += w < warp ? scan[w] : 0;
             before += scan[w];
         }
-        const Shares ctas(total, gridDim.x);
+        const Shares ctas(total, gridDim.x, p.by_ctas);
         cta_first = ctas.first(blockIdx.x);
         cta_stop = ctas.first(blockIdx.x + 1);
         const Shares warps(cta_stop - cta_first, S::kWarps);
@@ -795,7 +801,7 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
     Queries<D, HG> qs;
     bool fine = true;
     Segment last{-1, 0, 0, 0, 0, 0};
-    Crossing cross{-1, 0, 0, 0};
+    Crossing cross{-1, 0, 0, 0, 0, 0};
     int end_item = -1;
     while (at < stop && fine) {
         Span sp = span_of_length(p, len);
@@ -810,7 +816,7 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
         const int item0 = seq0 + ig * sp.tiles;
         const int n0 = at - item0;
         const int n1 = min(sp.tiles, stop - item0);
-        const int kvh = ig / p.groups, grp = ig - kvh * p.groups;
+        const int kvh = p.by_groups.of(ig), grp = ig - kvh * p.groups;
         const int head0 = kvh * p.rep + grp * S::kHeads;
         const int heads = min(S::kHeads, p.rep - grp * S::kHeads);
         // Page numbers of the next tiles, one lane each (a page of 128 tokens
@@ -877,12 +883,14 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
             good |= fetch(n0 + s, s) << (4 * s);
         if (n0 > 0 && at == cta_first) {
             // (while the first tile is on its way)
-            const Shares ctas(total, gridDim.x);
+            const Shares ctas(total, gridDim.x, p.by_ctas);
             const int first0 = ctas.first(blockIdx.x - 1);
             if (item0 >= first0) {
                 const int end = item0 + sp.tiles, cta1 = ctas.of(end - 1);
                 const int first1 = ctas.first(cta1);
-                cross.item = b * hg + ig;
+                cross.b = b;
+                cross.head0 = head0;
+                cross.heads = heads;
                 cross.parts = cta1 - int(blockIdx.x) + 2;
                 cross.warp0 = Shares(cta_first - first0, S::kWarps).of(item0 - first0);
                 cross.ended = end < first1 + Shares(ctas.first(cta1 + 1) - first1, S::kWarps).first(1);
@@ -1021,10 +1029,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     pdl_launch_dependents();
     const int c0 = blockIdx.x, h = blockIdx.y;
     const Crossing x = p.crossing[c0 + 1];
-    const int hg = p.c.kv_heads * p.groups;
-    const int b = x.item / hg, ig = x.item - b * hg;
-    const int kvh = ig / p.groups, grp = ig - kvh * p.groups;
-    if (x.item < 0 || h >= min(S::kHeads, p.rep - grp * S::kHeads))
+    if (x.b < 0 || h >= x.heads)
         return;
     // A CTA holds its part in the slot 1 of the first of its warps that worked
     // on it, or, where its first warp ended the item and went on, in slot 0.
@@ -1063,7 +1068,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     if (group == 0) {
         for (int i = 1; i < kGroups; ++i)
             r.add(vs[i][d / 2], mls[i]);
-        store_joined<D>(p, r, b, kvh * p.rep + grp * S::kHeads + h, d);
+        store_joined<D>(p, r, x.b, x.head0 + h, d);
     }
 }
 
@@ -1148,6 +1153,8 @@ cudaError_t launch_kv4_decode(const Kv4View &c, int D, const Kv4Query &q, const 
     p.crossing = reinterpret_cast<Crossing *>(ws);
     p.parts = reinterpret_cast<float *>(ws + plan.parts_at);
     p.rows = plan.rows;
+    p.by_groups = Divisor(plan.groups);
+    p.by_ctas = Divisor(plan.ctas);
     if (D == 128)
         return plan.hg == 1   ? launch<128, 1>(p, plan, stream)
                : plan.hg == 2 ? launch<128, 2>(p, plan, stream)
