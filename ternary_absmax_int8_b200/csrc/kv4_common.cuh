@@ -10,6 +10,7 @@
 // of tokens is one bulk copy.
 #pragma once
 
+#include "divisor.cuh"
 #include "tq_internal.h"
 
 namespace tq {
@@ -28,26 +29,6 @@ struct Kv4View {
     __host__ __device__ long long head_bytes() const
     {
         return (long long)(D + 4) << lg_ps;
-    }
-};
-
-// Division of whole numbers below 2^31 by d: with 2^(l-1) < d <= 2^l and
-// m = ceil(2^(31+l) / d), m d exceeds 2^(31+l) by less than 2^l, so that
-// x m / 2^(31+l) is above x / d by less than 1 / d.
-struct Divisor {
-    unsigned m;
-    int shift;
-
-    Divisor() = default;
-    explicit Divisor(int d) : m(0), shift(31)
-    {
-        while ((1ll << (shift - 31)) < d)
-            ++shift;
-        m = unsigned(((1ull << shift) + unsigned(d) - 1) / unsigned(d));
-    }
-    __device__ __forceinline__ int of(int x) const
-    {
-        return int((unsigned long long)unsigned(x) * m >> shift);
     }
 };
 

@@ -10,12 +10,13 @@
 // Bound by HBM at a prompt's length: every row is read and written once, with
 // 16-byte accesses, and a token's angles are computed once for all its heads
 // (they live in shared memory). 8192 tokens of 25 heads of 128, fp32 to bf16:
-// 27.8 us, 5.66 TB/s (86% of a plain copy). A CTA takes one token while tokens
+// 27.5 us, 5.71 TB/s (87% of a plain copy). A CTA takes one token while tokens
 // are few (a decode step of 16 is 2.1 us, with two tokens a CTA 2.9), two from 4
-// tokens per SM, where one leaves threads idle in the angles (30.0 us at 8192)
-// and four too few CTAs (29.4).
+// tokens per SM, where one leaves threads idle in the angles (30.0 us at 8192,
+// when two took 27.8) and four too few CTAs (29.4).
 #include <algorithm>
 
+#include "divisor.cuh"
 #include "quant_core.cuh"
 #include "tq_internal.h"
 
@@ -33,6 +34,7 @@ struct RopeParams {
     const float *inv_freq;
     int section_end[kRopeMaxAxes];
     int n, n_axes, T, D, rot, interleaved, tokens_per_cta;
+    Divisor by_half, by_units, by_heads;
 };
 
 __device__ __forceinline__ void load8(const RopeRows &r, long long at, float (&v)[8])
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     pdl_wait();
     pdl_launch_dependents();
     for (int j = threadIdx.x; j < tokens * half; j += kRopeThreads) {
-        const int t = j / half, i = j - t * half;
+        const int t = p.by_half.of(j), i = j - t * half;
         int a = 0;
         while (a + 1 < p.n_axes && i >= p.section_end[a])
             ++a;
@@ -93,8 +95,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     }
     __syncthreads();
     for (int j = threadIdx.x; j < tokens * heads * units; j += kRopeThreads) {
-        const int th = j / units, u = j - th * units;
-        const int t = th / heads, h = th - t * heads;
+        const int th = p.by_units.of(j), u = j - th * units;
+        const int t = p.by_heads.of(th), h = th - t * heads;
         int e = 0;
         while (e + 1 < p.n && h >= p.head0[e + 1])
             ++e;
@@ -165,6 +167,9 @@ cudaError_t launch_rope(const RopeRows *rows, int n, const int32_t *pos, long lo
     p.rot = rot;
     p.interleaved = interleaved;
     p.tokens_per_cta = T >= 4 * device_sm_count() ? 2 : 1;
+    p.by_half = Divisor(std::max(1, rot / 2));
+    p.by_units = Divisor((rot >> 4) + ((D - rot + 15) >> 4));
+    p.by_heads = Divisor(p.head0[n]);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned((T + p.tokens_per_cta - 1) / p.tokens_per_cta));
     cfg.blockDim = dim3(kRopeThreads);
