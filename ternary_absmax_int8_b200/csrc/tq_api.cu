@@ -503,7 +503,10 @@ tq_status check_kv4_query(const char *fn, const tq_kv4_cache *c, const tq_kv4_qu
     if (q->lse && !aligned(q->lse, 4))
         return fail(TQ_ERR_ALIGN, "%s: lse must be 4-byte aligned", fn);
     const long long packed = (long long)q->q_heads * c->head_dim;
-    *out = tq::Kv4Query{q->q, q->out, q->lse, 0, 0, q->q_heads, q->window, q->scale};
+    // A window of the whole table or more hides no key; one below that (less than
+    // 2^30) can be taken from a position, and a key from that, in 32 bits.
+    const int window = q->window >= c->max_pages * c->page_size ? 0 : q->window;
+    *out = tq::Kv4Query{q->q, q->out, q->lse, 0, 0, q->q_heads, window, q->scale};
     st = check_rows(fn, "q", q->q, q->q_stride, packed, 2, &out->q_stride);
     return st != TQ_OK ? st
                        : check_rows(fn, "out", q->out, q->out_stride, packed, 2, &out->out_stride);
