@@ -540,10 +540,13 @@ tq_status tq_kv4_append(const tq_kv4_cache *cache, const uint16_t *k_bf16,
  * j <= p, j > p - window where window > 0:
  *   z_j = scale * (q . k_j),  out = sum_j softmax(z)_j v_j,
  *   lse = log(sum_j exp(z_j))   (natural logarithm)
- * A query that sees nothing has out = 0 and lse = -infinity. Scores are fp32
- * numbers, of query values that are 0 or at least 2^-90 (no upper limit) with
- * |k| and scale |q| up to 2^90. A NaN or an infinity among a row's query
- * values, or a score beyond fp32's largest number, makes that row NaN.
+ * A query before position 0 (of an empty sequence, of more new tokens than the
+ * length holds) sees nothing: out = 0 and lse = -infinity, whatever its values.
+ * So has a query of finite values whose keys all lie in pages outside the cache.
+ * Scores are fp32 numbers, of query values that are 0 or at least 2^-90 (no
+ * upper limit) with |k| and scale |q| up to 2^90. From position 0 on a NaN or an
+ * infinity among a row's query values, or a score beyond fp32's largest number,
+ * makes that row NaN.
  * Roundings: scores and sums in fp32; a weight times its value's scale once to
  * fp16 (tq_kv4_decode, against the largest scale of 64 tokens) or bf16
  * (tq_kv4_prefill); out to bf16.

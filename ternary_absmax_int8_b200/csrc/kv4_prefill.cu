@@ -548,8 +548,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         if (n > 0 && s < nq) {
             const int twist = ((lane << 1) & 7) ^ ((lane & 4) ? 3 : 0);
             fine = mbar_wait_warp(&sh.bar.q_raw[warp], 0, p.c.err);
+            // (a row before position 0 sees nothing: were it NaN, its masked scores
+            // would be, so it counts as zeros)
             auto chunk = [&](int c) {
-                return real ? lds128(raw + (c << 4)) : make_uint4(0, 0, 0, 0);
+                return pos >= 0 ? lds128(raw + (c << 4)) : make_uint4(0, 0, 0, 0);
             };
             uint4 v[D / 8];
 #pragma unroll
