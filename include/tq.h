@@ -543,10 +543,11 @@ tq_status tq_kv4_append(const tq_kv4_cache *cache, const uint16_t *k_bf16,
  * A query before position 0 (of an empty sequence, of more new tokens than the
  * length holds) sees nothing: out = 0 and lse = -infinity, whatever its values.
  * So has a query of finite values whose keys all lie in pages outside the cache.
- * Scores are fp32 numbers, of query values that are 0 or at least 2^-90 (no
- * upper limit) with |k| and scale |q| up to 2^90. From position 0 on a NaN or an
- * infinity among a row's query values, or a score beyond fp32's largest number,
- * makes that row NaN.
+ * Scores are fp32 numbers (taken in base 2, 1.44 times z), of query values that
+ * are 0 or at least 2^-90 (no upper limit) with |k| and scale |q| up to 2^90 and
+ * their products up to 2^130. A largest score above fp32's numbers makes the row
+ * NaN; one below them counts as not seen. From position 0 on a NaN or an infinity
+ * among a row's query values makes that row NaN.
  * Roundings: scores and sums in fp32; a weight times its value's scale once to
  * fp16 (tq_kv4_decode, against the largest scale of 64 tokens) or bf16
  * (tq_kv4_prefill); out to bf16.

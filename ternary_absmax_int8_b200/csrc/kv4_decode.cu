@@ -465,8 +465,10 @@ __device__ __forceinline__ void tile_step(const uint8_t *stage, int lg_sps, int 
     uint32_t pb[kV][4][2];
     float c[HG];
 #pragma unroll
-    for (int j = 0; j < HG; ++j)
-        c[j] = r.m[j] == -INFINITY ? 0.0f : -r.m[j] * q.mul[j];
+    for (int j = 0; j < HG; ++j) {
+        const float top = r.m[j] * q.mul[j];
+        c[j] = top == -INFINITY ? 0.0f : -top;  // nothing seen, or nothing above -FLT_MAX
+    }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -539,15 +541,19 @@ __device__ __forceinline__ float2 value_pair(const Running<D, HG> &r, int j, int
     return make_float2(r.o[j / 2][i][j & 1], r.o[j / 2][i][2 + (j & 1)]);
 }
 
-// The sums of weights lie spread over the lanes of a column: add them up.
+// The sums of weights lie spread over the lanes of a column: add them up. Where
+// the largest score is above fp32's numbers no weight is known.
 template <int D, int HG>
-__device__ __forceinline__ void close_sums(Running<D, HG> &r)
+__device__ __forceinline__ void close_sums(Running<D, HG> &r, const Queries<D, HG> &q)
 {
 #pragma unroll
-    for (int j = 0; j < HG; ++j)
+    for (int j = 0; j < HG; ++j) {
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1)
             r.l[j] += __shfl_xor_sync(0xffffffffu, r.l[j], o);
+        if (r.m[j] * q.mul[j] == INFINITY)
+            r.l[j] = NAN;
+    }
 }
 
 // A part [heads][D + 2]: values, then the maximum (base 2) and the sum. For
@@ -914,7 +920,7 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
         }
         if (!fine)
             break;
-        close_sums<D, HG>(run);
+        close_sums<D, HG>(run, qs);
         at = item0 + n1;
         if (n0 == 0 && n1 == sp.tiles) {
             store_final<D, HG>(p, run, qs, b, head0, heads);

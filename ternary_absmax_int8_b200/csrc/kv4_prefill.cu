@@ -694,6 +694,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             tc_fence_before();
             warp_arrive(&sh.bar.p_full[s][half]);
         }
+        // A largest score above fp32's numbers: no weight is known.
+        if (m == INFINITY)
+            lsum = NAN;
         // Output rows (a row tile without keys, or without rows, has none).
         const float inv = lsum == 0.0f ? 0.0f : poisoned ? NAN : 1.0f / lsum;
         const long long token = u.start + tok;

@@ -52,3 +52,48 @@ def test_queries_before_position_0_see_nothing_whatever_they_hold(cuda_device):
         lse, rlse, ltol = (np.where(nan, 0, x) for x in (got[1], ref[1], ref[3]))
         assert_attention((got[0], lse), (ref[0], rlse, ref[2], ltol))
         assert tq.tq_device_error() == 0
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("D,rep", [(128, 4), (64, 7), (64, 16)])
+def test_scores_beyond_fp32(cuda_device, decode, D, rep):
+    """Keys whose scores are 0, 2^134 or -2^134 times a little: a row that sees one
+    of the large ones is NaN, those far below count as not seen, and the others
+    weigh the same. The weights are equal and exact, so the tolerance is that of
+    tests/_kv4.py without the part of the scores."""
+    rng = np.random.default_rng(32)
+    lens = [200, 200, 150, 300, 1, 1]
+    n = [1] * 6 if decode else [170, 30, 2, 5, 1, 1]
+    hk = 2
+    cache = Cache(rng, lens, hk, D, 32)
+    kind = [rng.integers(-1, 1, L) for L in lens]  # 0, or far below
+    kind[1][40] = 1                                # one far above
+    kind[2][:] = -1                                # nothing else
+    kind[3][:] = np.where(np.arange(300) < 131, -1, 0)
+    kind[4][:], kind[5][:] = 1, -1
+    for b, ks in enumerate(kind):
+        for j, x in enumerate(ks):
+            at = cache.table[b, j // 32], 0, slice(None), j % 32
+            cache.codes[at], cache.scales[at] = 7 * x, np.float32(2.0 ** 60)
+    c, keep = cache.on_gpu()
+    q = np.full((sum(n), hk * rep, D), 2.0 ** 66, np.float32)
+    out, lse = run_attention(c, keep, q, lens, n, 1.0, decode=decode)
+    t = 0
+    for b, nb in enumerate(n):
+        v = cache.rows(b, 1)
+        for p in range(lens[b] - nb, lens[b]):
+            seen = kind[b][:p + 1]
+            if (seen > 0).any():
+                assert np.isnan(out[t]).all() and np.isnan(lse[t]).all()
+            elif (seen < 0).all():
+                assert (out[t] == 0).all() and np.isneginf(lse[t]).all()
+            else:
+                vv = np.repeat(v[:, :p + 1][:, seen == 0], rep, 0)  # [heads, keys, D]
+                ref, A = vv.mean(1), np.abs(vv).mean(1)
+                tol = (2.0 ** -8 * np.abs(ref) + A * (2.0 ** -8 + 2.0 ** -12)
+                       + 2.0 ** -39 * vv.shape[1] * np.abs(vv).max())
+                assert (np.abs(out[t] - ref) <= tol).all()
+                want = np.log(vv.shape[1])
+                assert (np.abs(lse[t] - want) <= 2.0 ** -18 + 2.0 ** -22 * want).all()
+            t += 1
+    assert tq.tq_device_error() == 0
