@@ -138,14 +138,6 @@ __device__ Unit find_unit(const PrefillParams &p, int u, int *scratch)
     return Unit{-1, 0, 0, 0, 0};
 }
 
-// The first key that the window ending at position `pos` holds, or a number
-// below 0 where it reaches beyond the start. (Positions before 0 see nothing;
-// they are counted as 0, far below which the difference would wrap around.)
-__device__ __forceinline__ int window_start(int pos, int window)
-{
-    return max(pos, 0) - window + 1;
-}
-
 // Key tiles [first, last) of 128 that a unit's split works through.
 struct Tiles {
     int first, last;
@@ -157,8 +149,10 @@ __device__ __forceinline__ Tiles tiles_of(const PrefillParams &p, const Unit &u,
     const int last_row = min(u.row0 + kRows, u.n * p.rep) - 1;
     const int p0 = u.pos0 + p.by_rep.of(u.row0), p1 = u.pos0 + p.by_rep.of(last_row);
     Tiles t;
+    // (p0 may be 2^30 or more below 0 where tok_start names far more tokens than
+    // the call has: then p1 < 0, and there are no tiles whatever begin is)
     t.end = min(max(p1 + 1, 0), p.c.max_len());
-    t.begin = p.q.window > 0 ? max(0, window_start(p0, p.q.window)) : 0;
+    t.begin = p.q.window > 0 ? max(0, p0 - p.q.window + 1) : 0;
     const int a = t.begin / kKeys, n = max(0, (t.end + kKeys - 1) / kKeys - a);
     t.first = a + p.by_splits.of(n * split);  // (at most 2^23 tiles, 32 parts)
     t.last = a + p.by_splits.of(n * (split + 1));
@@ -530,13 +524,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     if (warp < 8) {
         // ---------------------------------------------------------- softmax
         const int s = warp >> 2;
-        const int pos = real ? u.pos0 + tok : -1;
-        const int low = p.q.window > 0 ? window_start(pos, p.q.window) : 0;  // first key seen
+        const int pos = real ? u.pos0 + tok : -1;  // -1: sees nothing
+        const int low = p.q.window > 0 ? pos - p.q.window + 1 : 0;  // first key seen
         // what all rows of the tile see: keys [low_max, pos_min]
         const int pos_min = u.pos0 + p.by_rep.of(u.row0 + s * 128);
         const int last = min(s * 128 + 127, rows - 1);
         const int low_max =
-            p.q.window > 0 ? window_start(u.pos0 + p.by_rep.of(u.row0 + last), p.q.window) : 0;
+            p.q.window > 0 ? u.pos0 + p.by_rep.of(u.row0 + last) - p.q.window + 1 : 0;
         const uint32_t lane_at = uint32_t((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_at + s * 128, to = tmem + lane_at + 256 + s * D;
         // The thread's query row as fp16 against its largest magnitude: 16 bytes at

@@ -2,6 +2,7 @@
 against 64 bits (tolerances: tests/_kv4.py)."""
 import numpy as np
 import pytest
+import torch
 
 import ternary_absmax_int8_b200 as tq
 from tests._kv4 import Cache, assert_attention, attention, queries, run_attention
@@ -22,6 +23,23 @@ def test_windows_beyond_the_table(cuda_device, decode, window):
     got = run_attention(c, keep, q, lens, n, 0.125, window, decode=decode)
     assert_attention(got, attention(cache, q, n, 0.125, window))
     assert tq.tq_device_error() == 0
+
+
+@pytest.mark.parametrize("window", [0, 5, 100, 2 ** 31 - 1])
+def test_rows_far_before_position_0(cuda_device, window):
+    """tok_start that names 2^31 - 1 tokens of which the call has five."""
+    rng = np.random.default_rng(33)
+    cache = Cache(rng, [100], 2, 64, 16)
+    c, keep = cache.on_gpu()
+    f = dict(device="cuda", dtype=torch.int32)
+    q = torch.from_numpy(queries(rng, 5, 4, 64)).cuda().bfloat16()
+    out, lse = torch.full_like(q, 7.0), torch.full((5, 4), 7.0, device="cuda")
+    size = tq.tq_kv4_prefill_workspace(c, 4, 5)
+    ws = torch.empty(max(16, size), dtype=torch.uint8, device="cuda")
+    tq.tq_kv4_prefill(c, q, torch.tensor([0, 2 ** 31 - 1], **f), torch.tensor([100], **f), out, lse,
+                      5, 4, 0.1, window, ws, size)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and torch.isneginf(lse).all() and tq.tq_device_error() == 0
 
 
 def test_queries_before_position_0_see_nothing_whatever_they_hold(cuda_device):
