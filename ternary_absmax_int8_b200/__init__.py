@@ -382,15 +382,28 @@ def _here(stream):
     return device, _stream(stream)
 
 
-def _gpu_ptr(t, size: int, device: int):
-    """Pointer of a tensor of `size`-byte elements on CUDA device `device`, the current one (an
-    int or None passes through); a tensor elsewhere is refused, as the kernel would run here."""
+# Element types that a pointer of each kind may come from (also plain whole numbers of its size,
+# where the bits are what counts); filled when the first tensor is met, as torch is imported late.
+_KINDS = {}
+
+
+def _kinds():
+    import torch
+    _KINDS.update(bf16=(torch.bfloat16, torch.int16, torch.uint16), f32=(torch.float32,),
+                  i32=(torch.int32, torch.uint32), u8=(torch.uint8, torch.int8))
+    return _KINDS
+
+
+def _gpu_ptr(t, kind: str, device: int):
+    """Pointer of a tensor of `kind` elements on CUDA device `device`, the current one (an int or
+    None passes through); one of another type would be misread, one elsewhere not be found here."""
     if t is None or isinstance(t, int):
         return t
-    if t.get_device() == device and t.element_size() == size:
+    kinds = (_KINDS or _kinds())[kind]
+    if t.get_device() == device and t.dtype in kinds:
         return t.data_ptr()
-    if t.element_size() != size:
-        raise TQError(4, f"a tensor of {size}-byte elements is wanted, not {t.dtype}")
+    if t.dtype not in kinds:
+        raise TQError(4, f"a tensor of {kinds[0]} is wanted, not {t.dtype}")
     raise TQError(4, f"a tensor on {t.device}: tensors must be on the current CUDA device")
 
 
@@ -400,8 +413,8 @@ def make_rope_rows(rows, head_dim: int):
     arr = (TqRopeRows * len(rows))()
     dev = _device()
     for e, r in zip(arr, rows):
-        e.x_bf16, e.x_f32 = _gpu_ptr(r.get("x_bf16"), 2, dev), _gpu_ptr(r.get("x_f32"), 4, dev)
-        e.y_bf16, e.y_f32 = _gpu_ptr(r.get("y_bf16"), 2, dev), _gpu_ptr(r.get("y_f32"), 4, dev)
+        e.x_bf16, e.x_f32 = _gpu_ptr(r.get("x_bf16"), "bf16", dev), _gpu_ptr(r.get("x_f32"), "f32", dev)
+        e.y_bf16, e.y_f32 = _gpu_ptr(r.get("y_bf16"), "bf16", dev), _gpu_ptr(r.get("y_f32"), "f32", dev)
         e.heads = int(r["heads"])
         e.x_stride = int(r.get("x_stride", 0)) or e.heads * int(head_dim)
         e.y_stride = int(r.get("y_stride", 0)) or e.heads * int(head_dim)
@@ -413,8 +426,8 @@ def tq_rope(rows, pos, inv_freq, sections, T: int, head_dim: int, rot_dim: int, 
     """Rotary positions of the rows in a make_rope_rows table; pos int32 [len(sections), T]."""
     dev, stream = _here(stream)
     n = len(sections)
-    _check(_load().tq_rope(rows, len(rows), _gpu_ptr(pos, 4, dev), int(pos_stride) or int(T),
-                           _gpu_ptr(inv_freq, 4, dev), (_i * n)(*sections), n, int(T), int(head_dim),
+    _check(_load().tq_rope(rows, len(rows), _gpu_ptr(pos, "i32", dev), int(pos_stride) or int(T),
+                           _gpu_ptr(inv_freq, "f32", dev), (_i * n)(*sections), n, int(T), int(head_dim),
                            int(rot_dim), int(flags), stream))
 
 
@@ -427,7 +440,7 @@ def make_kv4_cache(pages=None, page_table=None, num_pages: int = 0, page_size: i
                    page_stride: int = 0) -> TqKv4Cache:
     """Describe a 4-bit key/value cache. It holds pointers only: keep the tensors."""
     dev = _device()
-    return TqKv4Cache(_gpu_ptr(pages, 1, dev), _gpu_ptr(page_table, 4, dev), int(page_stride),
+    return TqKv4Cache(_gpu_ptr(pages, "u8", dev), _gpu_ptr(page_table, "i32", dev), int(page_stride),
                       int(num_pages), int(page_size), int(kv_heads), int(head_dim), int(batch),
                       int(max_pages))
 
@@ -436,9 +449,9 @@ def tq_kv4_append(cache, k_bf16, v_bf16, k_f32, v_f32, tok_start, lens, T: int, 
                   v_stride: int = 0, stream=None) -> None:
     """Quantise new keys and values into the cache's pages (one of the two pairs)."""
     dev, stream = _here(stream)
-    _check(_load().tq_kv4_append(ctypes.byref(cache), _gpu_ptr(k_bf16, 2, dev), _gpu_ptr(v_bf16, 2, dev),
-                                 _gpu_ptr(k_f32, 4, dev), _gpu_ptr(v_f32, 4, dev), int(k_stride),
-                                 int(v_stride), _gpu_ptr(tok_start, 4, dev), _gpu_ptr(lens, 4, dev), int(T),
+    _check(_load().tq_kv4_append(ctypes.byref(cache), _gpu_ptr(k_bf16, "bf16", dev), _gpu_ptr(v_bf16, "bf16", dev),
+                                 _gpu_ptr(k_f32, "f32", dev), _gpu_ptr(v_f32, "f32", dev), int(k_stride),
+                                 int(v_stride), _gpu_ptr(tok_start, "i32", dev), _gpu_ptr(lens, "i32", dev), int(T),
                                  stream))
 
 
@@ -456,7 +469,7 @@ def tq_kv4_prefill_workspace(cache, q_heads: int, T: int) -> int:
 
 
 def _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride):
-    return ctypes.byref(TqKv4Query(_gpu_ptr(q, 2, dev), _gpu_ptr(out, 2, dev), _gpu_ptr(lse, 4, dev),
+    return ctypes.byref(TqKv4Query(_gpu_ptr(q, "bf16", dev), _gpu_ptr(out, "bf16", dev), _gpu_ptr(lse, "f32", dev),
                                    int(q_stride), int(out_stride), int(q_heads),
                                    int(window), float(scale), 0))
 
@@ -467,8 +480,8 @@ def tq_kv4_decode(cache, q, lens, out, lse, q_heads: int, scale: float, window: 
     """Attention of one new token per sequence over the cache."""
     dev, stream = _here(stream)
     query = _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride)
-    _check(_load().tq_kv4_decode(ctypes.byref(cache), query, _gpu_ptr(lens, 4, dev),
-                                 _gpu_ptr(workspace, 1, dev), int(workspace_bytes), stream))
+    _check(_load().tq_kv4_decode(ctypes.byref(cache), query, _gpu_ptr(lens, "i32", dev),
+                                 _gpu_ptr(workspace, "u8", dev), int(workspace_bytes), stream))
 
 
 def tq_kv4_prefill(cache, q, tok_start, lens, out, lse, T: int, q_heads: int, scale: float,
@@ -477,6 +490,6 @@ def tq_kv4_prefill(cache, q, tok_start, lens, out, lse, T: int, q_heads: int, sc
     """Attention of any number of new tokens per sequence over the cache."""
     dev, stream = _here(stream)
     query = _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride)
-    _check(_load().tq_kv4_prefill(ctypes.byref(cache), query, _gpu_ptr(tok_start, 4, dev),
-                                  _gpu_ptr(lens, 4, dev), int(T), _gpu_ptr(workspace, 1, dev),
+    _check(_load().tq_kv4_prefill(ctypes.byref(cache), query, _gpu_ptr(tok_start, "i32", dev),
+                                  _gpu_ptr(lens, "i32", dev), int(T), _gpu_ptr(workspace, "u8", dev),
                                   int(workspace_bytes), stream))
