@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 __all__ = [
     "TQError", "TQ_STACK_OVERLAP_PREV", "TQ_STACK_QUANTIZE", "TQ_STACK_RMSNORM",
@@ -372,39 +373,59 @@ def _device() -> int:
 def _here(stream):
     """The current CUDA device and the handle of `stream` (of the current one if None): what a
     call needs to know, looked up once."""
-    import torch
-    if not torch.cuda.is_initialized():
+    torch = sys.modules.get("torch")
+    if torch is None or not torch.cuda.is_initialized():
         return _device(), _stream(stream)
-    device = torch.cuda.current_device()
+    # (torch's own functions for these look up again whether CUDA is up, and build a Stream)
+    device = torch._C._cuda_getDevice()
     if stream is None:
-        # without building a Stream object around it
         return device, torch._C._cuda_getCurrentRawStream(device)
     return device, _stream(stream)
 
 
 # Element types that a pointer of each kind may come from (also plain whole numbers of its size,
 # where the bits are what counts); filled when the first tensor is met, as torch is imported late.
-_KINDS = {}
+_BF16, _F32, _I32, _U8 = [], [], [], []
 
 
-def _kinds():
-    import torch
-    _KINDS.update(bf16=(torch.bfloat16, torch.int16, torch.uint16), f32=(torch.float32,),
-                  i32=(torch.int32, torch.uint32), u8=(torch.uint8, torch.int8))
-    return _KINDS
-
-
-def _gpu_ptr(t, kind: str, device: int):
-    """Pointer of a tensor of `kind` elements on CUDA device `device`, the current one (an int or
-    None passes through); one of another type would be misread, one elsewhere not be found here."""
+def _gpu_ptr(t, kinds, device: int, stride: int = 0):
+    """Pointer of a tensor of one of the types `kinds` on CUDA device `device`, the current one (an
+    int or None passes through); one of another type would be misread, one elsewhere not be found
+    here. Its elements must follow one another, but for rows that are `stride` elements apart."""
     if t is None or isinstance(t, int):
         return t
-    kinds = (_KINDS or _kinds())[kind]
-    if t.get_device() == device and t.dtype in kinds:
+    if t.dtype in kinds and t.get_device() == device and (t.is_contiguous() or _rows(t, stride)):
         return t.data_ptr()
+    if not kinds:
+        import torch
+        _BF16[:] = torch.bfloat16, torch.int16, torch.uint16
+        _F32[:] = torch.float32,
+        _I32[:] = torch.int32, torch.uint32
+        _U8[:] = torch.uint8, torch.int8
+        return _gpu_ptr(t, kinds, device, stride)
     if t.dtype not in kinds:
         raise TQError(4, f"a tensor of {kinds[0]} is wanted, not {t.dtype}")
-    raise TQError(4, f"a tensor on {t.device}: tensors must be on the current CUDA device")
+    if t.get_device() != device:
+        raise TQError(4, f"a tensor on {t.device}: tensors must be on the current CUDA device")
+    raise TQError(4, f"a view of shape {tuple(t.shape)}, strides {tuple(t.stride())}: it must be "
+                     "contiguous" + (f" or of rows {stride} elements apart" if stride else ""))
+
+
+def _rows(t, stride: int) -> bool:
+    """Whether t is rows that lie `stride` elements apart, each contiguous, in as many leading
+    and trailing dimensions as it may be."""
+    if t.dim() < 2 or (t.shape[-1] != 1 and t.stride(-1) != 1):
+        return False
+    want, inner = 1, True
+    for size, step in zip(reversed(t.shape), reversed(t.stride())):
+        if size == 1:
+            continue
+        if step != want:
+            if not inner or step != stride or stride == 0:
+                return False
+            want, inner = stride, False
+        want *= size
+    return True
 
 
 def make_rope_rows(rows, head_dim: int):
@@ -413,11 +434,13 @@ def make_rope_rows(rows, head_dim: int):
     arr = (TqRopeRows * len(rows))()
     dev = _device()
     for e, r in zip(arr, rows):
-        e.x_bf16, e.x_f32 = _gpu_ptr(r.get("x_bf16"), "bf16", dev), _gpu_ptr(r.get("x_f32"), "f32", dev)
-        e.y_bf16, e.y_f32 = _gpu_ptr(r.get("y_bf16"), "bf16", dev), _gpu_ptr(r.get("y_f32"), "f32", dev)
         e.heads = int(r["heads"])
         e.x_stride = int(r.get("x_stride", 0)) or e.heads * int(head_dim)
         e.y_stride = int(r.get("y_stride", 0)) or e.heads * int(head_dim)
+        e.x_bf16 = _gpu_ptr(r.get("x_bf16"), _BF16, dev, e.x_stride)
+        e.x_f32 = _gpu_ptr(r.get("x_f32"), _F32, dev, e.x_stride)
+        e.y_bf16 = _gpu_ptr(r.get("y_bf16"), _BF16, dev, e.y_stride)
+        e.y_f32 = _gpu_ptr(r.get("y_f32"), _F32, dev, e.y_stride)
     return arr
 
 
@@ -426,9 +449,10 @@ def tq_rope(rows, pos, inv_freq, sections, T: int, head_dim: int, rot_dim: int, 
     """Rotary positions of the rows in a make_rope_rows table; pos int32 [len(sections), T]."""
     dev, stream = _here(stream)
     n = len(sections)
-    _check(_load().tq_rope(rows, len(rows), _gpu_ptr(pos, "i32", dev), int(pos_stride) or int(T),
-                           _gpu_ptr(inv_freq, "f32", dev), (_i * n)(*sections), n, int(T), int(head_dim),
-                           int(rot_dim), int(flags), stream))
+    pos_stride = int(pos_stride) or int(T)
+    _check(_load().tq_rope(rows, len(rows), _gpu_ptr(pos, _I32, dev, pos_stride), pos_stride,
+                           _gpu_ptr(inv_freq, _F32, dev), (_i * n)(*sections), n, int(T),
+                           int(head_dim), int(rot_dim), int(flags), stream))
 
 
 def tq_kv4_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
@@ -440,7 +464,8 @@ def make_kv4_cache(pages=None, page_table=None, num_pages: int = 0, page_size: i
                    page_stride: int = 0) -> TqKv4Cache:
     """Describe a 4-bit key/value cache. It holds pointers only: keep the tensors."""
     dev = _device()
-    return TqKv4Cache(_gpu_ptr(pages, "u8", dev), _gpu_ptr(page_table, "i32", dev), int(page_stride),
+    return TqKv4Cache(_gpu_ptr(pages, _U8, dev, page_stride),
+                      _gpu_ptr(page_table, _I32, dev, max_pages), int(page_stride),
                       int(num_pages), int(page_size), int(kv_heads), int(head_dim), int(batch),
                       int(max_pages))
 
@@ -449,10 +474,11 @@ def tq_kv4_append(cache, k_bf16, v_bf16, k_f32, v_f32, tok_start, lens, T: int, 
                   v_stride: int = 0, stream=None) -> None:
     """Quantise new keys and values into the cache's pages (one of the two pairs)."""
     dev, stream = _here(stream)
-    _check(_load().tq_kv4_append(ctypes.byref(cache), _gpu_ptr(k_bf16, "bf16", dev), _gpu_ptr(v_bf16, "bf16", dev),
-                                 _gpu_ptr(k_f32, "f32", dev), _gpu_ptr(v_f32, "f32", dev), int(k_stride),
-                                 int(v_stride), _gpu_ptr(tok_start, "i32", dev), _gpu_ptr(lens, "i32", dev), int(T),
-                                 stream))
+    _check(_load().tq_kv4_append(
+        ctypes.byref(cache), _gpu_ptr(k_bf16, _BF16, dev, k_stride),
+        _gpu_ptr(v_bf16, _BF16, dev, v_stride), _gpu_ptr(k_f32, _F32, dev, k_stride),
+        _gpu_ptr(v_f32, _F32, dev, v_stride), int(k_stride), int(v_stride),
+        _gpu_ptr(tok_start, _I32, dev), _gpu_ptr(lens, _I32, dev), int(T), stream))
 
 
 def tq_kv4_decode_workspace(cache, q_heads: int) -> int:
@@ -469,9 +495,10 @@ def tq_kv4_prefill_workspace(cache, q_heads: int, T: int) -> int:
 
 
 def _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride):
-    return ctypes.byref(TqKv4Query(_gpu_ptr(q, "bf16", dev), _gpu_ptr(out, "bf16", dev), _gpu_ptr(lse, "f32", dev),
-                                   int(q_stride), int(out_stride), int(q_heads),
-                                   int(window), float(scale), 0))
+    return ctypes.byref(TqKv4Query(_gpu_ptr(q, _BF16, dev, q_stride),
+                                   _gpu_ptr(out, _BF16, dev, out_stride),
+                                   _gpu_ptr(lse, _F32, dev), int(q_stride), int(out_stride),
+                                   int(q_heads), int(window), float(scale), 0))
 
 
 def tq_kv4_decode(cache, q, lens, out, lse, q_heads: int, scale: float, window: int = 0,
@@ -480,8 +507,8 @@ def tq_kv4_decode(cache, q, lens, out, lse, q_heads: int, scale: float, window: 
     """Attention of one new token per sequence over the cache."""
     dev, stream = _here(stream)
     query = _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride)
-    _check(_load().tq_kv4_decode(ctypes.byref(cache), query, _gpu_ptr(lens, "i32", dev),
-                                 _gpu_ptr(workspace, "u8", dev), int(workspace_bytes), stream))
+    _check(_load().tq_kv4_decode(ctypes.byref(cache), query, _gpu_ptr(lens, _I32, dev),
+                                 _gpu_ptr(workspace, _U8, dev), int(workspace_bytes), stream))
 
 
 def tq_kv4_prefill(cache, q, tok_start, lens, out, lse, T: int, q_heads: int, scale: float,
@@ -490,6 +517,6 @@ def tq_kv4_prefill(cache, q, tok_start, lens, out, lse, T: int, q_heads: int, sc
     """Attention of any number of new tokens per sequence over the cache."""
     dev, stream = _here(stream)
     query = _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride)
-    _check(_load().tq_kv4_prefill(ctypes.byref(cache), query, _gpu_ptr(tok_start, "i32", dev),
-                                  _gpu_ptr(lens, "i32", dev), int(T), _gpu_ptr(workspace, "u8", dev),
-                                  int(workspace_bytes), stream))
+    _check(_load().tq_kv4_prefill(ctypes.byref(cache), query, _gpu_ptr(tok_start, _I32, dev),
+                                  _gpu_ptr(lens, _I32, dev), int(T),
+                                  _gpu_ptr(workspace, _U8, dev), int(workspace_bytes), stream))

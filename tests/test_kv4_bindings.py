@@ -60,3 +60,62 @@ def test_other_types_are_refused(name, dtype):
     with pytest.raises(tq.TQError) as e:
         calls({name: t(dtype)})
     assert e.value.name == "TQ_ERR_VALUE" and str(dtype) in str(e.value)
+
+
+def wide(dtype, T, columns, rows=()):
+    """[T, columns] of rows of 1000 elements, or in the dimensions `rows` + columns."""
+    x = torch.zeros((T, 1000), dtype=dtype)[:, 8:8 + columns]
+    return x.unflatten(1, rows) if rows else x
+
+
+def test_rows_of_a_wider_tensor():
+    """Views whose rows lie as far apart as the call is told."""
+    for x in (wide(torch.bfloat16, 3, 128), wide(torch.bfloat16, 3, 128, (2, 64)),
+              torch.zeros((2, 3, 1000), dtype=torch.bfloat16)[..., :64],
+              wide(torch.bfloat16, 1, 128), torch.zeros((3, 1000), dtype=torch.bfloat16)):
+        c = cache()
+        tq.tq_kv4_append(c, x, x, None, None, None, None, 0, k_stride=1000, v_stride=1000)
+        tq.tq_kv4_decode(c, x, None, x, None, 1, 0.1, q_stride=1000, out_stride=1000)
+        tq.tq_kv4_prefill(c, x, None, None, x, None, 0, 1, 0.1, q_stride=1000, out_stride=1000)
+        tq.make_rope_rows([dict(x_bf16=x, y_bf16=x, heads=1, x_stride=1000, y_stride=1000)], 64)
+    pos = torch.zeros((3, 50), dtype=torch.int32)
+    for p, T, stride in ((pos[:, :7], 7, 50), (pos[:, 4:5], 1, 50), (pos[:1, 3:9], 6, 0),
+                         (pos[0], 50, 0), (pos, 50, 0), (pos[::2, :2], 2, 100)):
+        tq.tq_rope(tq.make_rope_rows([], 64), p, None, [32], T, 64, 64, pos_stride=stride)
+    tq.make_kv4_cache(page_table=torch.zeros((4, 20), dtype=torch.int32)[:, :7], max_pages=20)
+    tq.make_kv4_cache(pages=torch.zeros((4, 2000), dtype=torch.uint8)[:, :1088], page_stride=2000)
+
+
+@pytest.mark.parametrize("stride", [0, 64, 128, 999])
+def test_views_that_would_be_misread_are_refused(stride):
+    """Rows at another distance than the call is told, and elements that do not
+    follow one another."""
+    def refused(fn, *a, **kw):
+        with pytest.raises(tq.TQError) as e:
+            fn(*a, **kw)
+        assert e.value.name == "TQ_ERR_VALUE" and "view" in str(e.value)
+
+    c, none = cache(), [None] * 4
+    for x in (wide(torch.bfloat16, 3, 128), wide(torch.bfloat16, 3, 128, (2, 64)),
+              torch.zeros((8, 4, 64), dtype=torch.bfloat16).transpose(0, 1),
+              torch.zeros((3, 128), dtype=torch.bfloat16)[:, ::2],
+              torch.zeros((1, 64), dtype=torch.bfloat16).expand(3, 64)):
+        refused(tq.tq_kv4_append, c, x, None, *none, 0, k_stride=stride)
+        refused(tq.tq_kv4_append, c, None, x, *none, 0, v_stride=stride)
+        refused(tq.tq_kv4_decode, c, x, *none[:3], 1, 0.1, q_stride=stride)
+        refused(tq.tq_kv4_decode, c, None, None, x, None, 1, 0.1, out_stride=stride)
+        refused(tq.tq_kv4_prefill, c, x, *none, 0, 1, 0.1, q_stride=stride)
+        for n in ("x", "y"):
+            refused(tq.make_rope_rows, [{n + "_bf16": x, "heads": 1, n + "_stride": stride}], 64)
+    i = torch.zeros((4, 20), dtype=torch.int32)
+    refused(tq.make_kv4_cache, page_table=i[:, :7], max_pages=7)
+    refused(tq.make_kv4_cache, page_table=i.t(), max_pages=20)
+    refused(tq.make_kv4_cache, pages=torch.zeros((4, 2000), dtype=torch.uint8)[:, :1088])
+    for p, T in ((i[0, ::2], 10), (i[:, :7], 7), (i[0, :4:2], 2), (i[:1, :4:2], 2)):
+        refused(tq.tq_rope, tq.make_rope_rows([], 64), p, None, [32], T, 64, 64)
+    for lens in (i[:, 0], i[0, ::3]):
+        refused(tq.tq_kv4_append, c, *none, None, lens, 0)
+        refused(tq.tq_kv4_append, c, *none, lens, None, 0)
+        refused(tq.tq_kv4_decode, c, None, lens, None, None, 1, 0.1)
+    refused(tq.tq_kv4_decode, c, None, None, None, torch.zeros(4, 8)[:, :4], 1, 0.1)
+    refused(tq.tq_rope, tq.make_rope_rows([], 64), None, torch.zeros(64)[::2], [32], 0, 64, 64)
