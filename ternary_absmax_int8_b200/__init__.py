@@ -428,6 +428,22 @@ def _rows(t, stride: int) -> bool:
     return True
 
 
+def _on(device: int, described, tensors):
+    """A description that names `tensors`, which are on `device`. (Of addresses that are given as
+    whole numbers the device is the caller's business.)"""
+    if any(hasattr(t, "data_ptr") for t in tensors):
+        described.device = device
+    return described
+
+
+def _same_device(described, device: int):
+    """Refuse a description whose tensors are on another device than the current one."""
+    made = getattr(described, "device", device)
+    if made != device:
+        raise TQError(4, f"described on device {made}, called on {device}: tensors must be on the "
+                         "current CUDA device")
+
+
 def make_rope_rows(rows, head_dim: int):
     """A table of ``tq_rope_rows`` from dicts with the keys x_bf16 or x_f32, y_bf16 or y_f32,
     heads and, for rows that are not packed, x_stride and y_stride (values between tokens)."""
@@ -441,13 +457,14 @@ def make_rope_rows(rows, head_dim: int):
         e.x_f32 = _gpu_ptr(r.get("x_f32"), _F32, dev, e.x_stride)
         e.y_bf16 = _gpu_ptr(r.get("y_bf16"), _BF16, dev, e.y_stride)
         e.y_f32 = _gpu_ptr(r.get("y_f32"), _F32, dev, e.y_stride)
-    return arr
+    return _on(dev, arr, [t for r in rows for t in r.values()])
 
 
 def tq_rope(rows, pos, inv_freq, sections, T: int, head_dim: int, rot_dim: int, flags: int = 0,
             pos_stride: int = 0, stream=None) -> None:
     """Rotary positions of the rows in a make_rope_rows table; pos int32 [len(sections), T]."""
     dev, stream = _here(stream)
+    _same_device(rows, dev)
     n = len(sections)
     pos_stride = int(pos_stride) or int(T)
     _check(_load().tq_rope(rows, len(rows), _gpu_ptr(pos, _I32, dev, pos_stride), pos_stride,
@@ -464,16 +481,17 @@ def make_kv4_cache(pages=None, page_table=None, num_pages: int = 0, page_size: i
                    page_stride: int = 0) -> TqKv4Cache:
     """Describe a 4-bit key/value cache. It holds pointers only: keep the tensors."""
     dev = _device()
-    return TqKv4Cache(_gpu_ptr(pages, _U8, dev, page_stride),
-                      _gpu_ptr(page_table, _I32, dev, max_pages), int(page_stride),
-                      int(num_pages), int(page_size), int(kv_heads), int(head_dim), int(batch),
-                      int(max_pages))
+    return _on(dev, TqKv4Cache(
+        _gpu_ptr(pages, _U8, dev, page_stride), _gpu_ptr(page_table, _I32, dev, max_pages),
+        int(page_stride), int(num_pages), int(page_size), int(kv_heads), int(head_dim),
+        int(batch), int(max_pages)), (pages, page_table))
 
 
 def tq_kv4_append(cache, k_bf16, v_bf16, k_f32, v_f32, tok_start, lens, T: int, k_stride: int = 0,
                   v_stride: int = 0, stream=None) -> None:
     """Quantise new keys and values into the cache's pages (one of the two pairs)."""
     dev, stream = _here(stream)
+    _same_device(cache, dev)
     _check(_load().tq_kv4_append(
         ctypes.byref(cache), _gpu_ptr(k_bf16, _BF16, dev, k_stride),
         _gpu_ptr(v_bf16, _BF16, dev, v_stride), _gpu_ptr(k_f32, _F32, dev, k_stride),
@@ -506,6 +524,7 @@ def tq_kv4_decode(cache, q, lens, out, lse, q_heads: int, scale: float, window: 
                   out_stride: int = 0, stream=None) -> None:
     """Attention of one new token per sequence over the cache."""
     dev, stream = _here(stream)
+    _same_device(cache, dev)
     query = _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride)
     _check(_load().tq_kv4_decode(ctypes.byref(cache), query, _gpu_ptr(lens, _I32, dev),
                                  _gpu_ptr(workspace, _U8, dev), int(workspace_bytes), stream))
@@ -516,6 +535,7 @@ def tq_kv4_prefill(cache, q, tok_start, lens, out, lse, T: int, q_heads: int, sc
                    out_stride: int = 0, stream=None) -> None:
     """Attention of any number of new tokens per sequence over the cache."""
     dev, stream = _here(stream)
+    _same_device(cache, dev)
     query = _kv4_query(dev, q, out, lse, q_heads, scale, window, q_stride, out_stride)
     _check(_load().tq_kv4_prefill(ctypes.byref(cache), query, _gpu_ptr(tok_start, _I32, dev),
                                   _gpu_ptr(lens, _I32, dev), int(T),

@@ -119,3 +119,30 @@ def test_views_that_would_be_misread_are_refused(stride):
         refused(tq.tq_kv4_decode, c, None, lens, None, None, 1, 0.1)
     refused(tq.tq_kv4_decode, c, None, None, None, torch.zeros(4, 8)[:, :4], 1, 0.1)
     refused(tq.tq_rope, tq.make_rope_rows([], 64), None, torch.zeros(64)[::2], [32], 0, 64, 64)
+
+
+def test_descriptions_of_another_device_are_refused(monkeypatch):
+    """A cache or rows described while another device was the current one."""
+    c = cache(pages=t(torch.uint8), page_table=4096)
+    rows = tq.make_rope_rows([dict(heads=0, y_f32=t(torch.float32))], 64)
+    none = [None] * 6
+
+    def call(c, rows):
+        return [lambda: tq.tq_rope(rows, None, None, [32], 0, 64, 64),
+                lambda: tq.tq_kv4_append(c, *none, 0),
+                lambda: tq.tq_kv4_decode(c, *none[:4], 1, 0.1),
+                lambda: tq.tq_kv4_prefill(c, *none[:5], 0, 1, 0.1)]
+
+    for f in call(c, rows):
+        f()
+    monkeypatch.setattr(tq, "_here", lambda stream: (1, 0))
+    for f in call(c, rows):
+        with pytest.raises(tq.TQError) as e:
+            f()
+        assert e.value.name == "TQ_ERR_VALUE" and "device" in str(e.value)
+    # addresses as whole numbers, structs filled in by hand: the caller's business
+    monkeypatch.setattr(tq, "_device", lambda: 0)
+    for f in call(cache(pages=4096, page_table=4096), tq.make_rope_rows([dict(heads=0, x_f32=64)], 64)):
+        f()
+    for f in call(tq.TqKv4Cache(page_size=16, kv_heads=1, head_dim=64), (tq.TqRopeRows * 1)()):
+        f()
