@@ -907,9 +907,16 @@ __global__ void __launch_bounds__(DecodeShape<D, HG>::kWarps * 32, 1)
 #pragma unroll 1
         for (int n = n0, s = 0; n < n1; ++n, s = s + 1 == S::kStages ? 0 : s + 1) {
             fine = mbar_wait_warp(&bars[warp][s], (phase >> s) & 1u, p.c.err);
-            phase ^= 1u << s;
-            if (!fine)
+            if (!fine) {
+                // The merge writes where the rings are, and the CTA may retire: not
+                // while copies of this and the next tiles are on their way.
+                for (int i = n; i < n1 && i < n + S::kStages; ++i) {
+                    mbar_wait_warp(&bars[warp][s], (phase >> s) & 1u, p.c.err);
+                    s = s + 1 == S::kStages ? 0 : s + 1;
+                }
                 break;
+            }
+            phase ^= 1u << s;
             const uint8_t *stage = ring + s * S::kStageBytes;
             const int j0 = (sp.tile0 + n) * kTile;
             const uint32_t here = (good >> (4 * s)) & 15u;
