@@ -542,6 +542,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         if (n > 0 && s < nq) {
             const int twist = ((lane << 1) & 7) ^ ((lane & 4) ? 3 : 0);
             fine = mbar_wait_warp(&sh.bar.q_raw[warp], 0, p.c.err);
+            if (!fine)  // (the CTA does not retire under the warp's copies)
+                mbar_wait_warp(&sh.bar.q_raw[warp], 0, p.c.err);
             // (a row before position 0 sees nothing: were it NaN, its masked scores
             // would be, so it counts as zeros)
             auto chunk = [&](int c) {
@@ -808,8 +810,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             }
         };
         bool fine = true;
+        int j = 0;
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
+        for (; j < n; ++j) {
             const int st = j & 1, slot = j % kScaleSlots, parity = (j >> 1) & 1;
             fine = (j < 2 || mbar_wait_warp(&sh.bar.k_empty[st], parity ^ 1, p.c.err)) &&
                    mbar_wait_warp(&sh.bar.packed_full[0][st], parity, p.c.err);
@@ -873,6 +876,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             if (lane == 0)
                 mbar_arrive(&sh.bar.packed_empty[1][st]);
         }
+        // Where a wait gave up, the CTA does not retire under the copies that may
+        // be on their way: this tile's and the next one's.
+        if (!fine)
+            for (int h = 2 * j; h < min(2 * j + 4, 2 * n); ++h)
+                mbar_wait_warp(&sh.bar.packed_full[h & 1][(h >> 1) & 1], (h >> 2) & 1, p.c.err);
     } else {
         // -------------------------------------------------------------- MMAs
         // One warp per row tile: a product is queued only a few deep, so what
@@ -953,6 +961,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                     if (j + 3 < n && lead)
                         umma_commit(&sh.bar.k_empty[st ^ 1]);
                 }
+            }
+            // Where a wait gave up, the tensor memory is not freed, nor does the CTA
+            // retire, under the products that were issued.
+            if (!fine) {
+                if (lead)
+                    umma_commit(&sh.bar.o_final[s]);
+                mbar_wait_warp(&sh.bar.o_final[s], 0, p.c.err);
             }
         }
         // ------------------------------------------------------------ copies
