@@ -115,3 +115,68 @@ def test_scores_beyond_fp32(cuda_device, decode, D, rep):
                 assert (np.abs(lse[t] - want) <= 2.0 ** -18 + 2.0 ** -22 * want).all()
             t += 1
     assert tq.tq_device_error() == 0
+
+
+def without(cache, q, n, scale, window, gone):
+    """tests/_kv4.py's attention, of sequences whose keys gone[b] are not there."""
+    class Rest:
+        hk, lens = cache.hk, cache.lens
+
+        @staticmethod
+        def rows(b, which):
+            x = cache.rows(b, which).copy()
+            x[:, gone[b][:x.shape[1]]] = 0
+            return x
+
+    out, lse, tol, ltol = attention(Rest, q, n, scale, window)
+    rep, t = q.shape[1] // cache.hk, 0
+    for b, nb in enumerate(n):
+        k, v = (cache.rows(b, w) for w in (0, 1))
+        for p in range(cache.lens[b] - nb, cache.lens[b]):
+            seen = np.arange(k.shape[1])
+            seen = seen[(seen <= p) & (seen > p - (window or p + 1)) & ~gone[b][:len(seen)]]
+            for h in range(q.shape[1]):
+                out[t, h], lse[t, h] = 0, -np.inf
+                if len(seen):
+                    z = scale * (k[h // rep, seen] @ q[t, h].astype(np.float64))
+                    lse[t, h] = z.max() + np.log(np.exp(z - z.max()).sum())
+                    w, vv = np.exp(z - lse[t, h]), v[h // rep, seen]
+                    out[t, h] = w @ vv
+                    # (attention's bound with this A; its dz is of all keys that are left)
+                    A = w @ np.abs(vv)
+                    tol[t, h] = (2.0 ** -8 * np.abs(out[t, h]) + 2.0 ** -39 * len(vv) * np.abs(vv).max()
+                                 + A * (2.0 ** -8 + 2 * (ltol[t, h] - 2.0 ** -18) + 2.0 ** -12) + 1e-30)
+            t += 1
+    return out, lse, tol, ltol
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("D,ps,window", [(64, 32, 0), (128, 16, 0), (128, 128, 0), (64, 64, 90)])
+def test_keys_of_pages_outside_the_cache_are_left_out(cuda_device, decode, D, ps, window):
+    """The sequences that name such pages: their other keys count, a row without any
+    is 0 and -infinity; and lengths beyond the table are cut to it."""
+    rng = np.random.default_rng(34)
+    lens, n = [300, 130, 2, 256], ([1] * 4 if decode else [120, 30, 2, 3])
+    cache = Cache(rng, lens, 2, D, ps, max_pages=384 // ps)
+    gone = [np.zeros(384, bool) for _ in lens]
+    good = cache.table.copy()
+    for b, page, name in ((0, 0, -1), (0, 200 // ps, cache.num_pages), (0, 299 // ps, 2 ** 31 - 1),
+                          (1, 0, -2 ** 31), (2, 0, cache.num_pages + 7)):
+        cache.table[b, page] = name
+        gone[b][page * ps:(page + 1) * ps] = True
+    c, keep = cache.on_gpu()
+    q = queries(rng, sum(n), 8, D)
+    got = run_attention(c, keep, q, lens, n, 0.1, window, decode=decode)
+    assert tq.tq_device_error(reset=True) == 2
+    cache.table = good
+    assert_attention(got, without(cache, q, n, 0.1, window, gone))
+
+    cut = [384, 40]
+    cache = Cache(rng, cut, 2, D, ps, max_pages=384 // ps)
+    c, keep = cache.on_gpu()
+    n = [1, 1] if decode else [150, 40]
+    q = queries(rng, sum(n), 8, D)
+    for beyond in (385, 2 ** 31 - 1):
+        got = run_attention(c, keep, q, [beyond, 40], n, 0.1, window, decode=decode)
+        assert tq.tq_device_error(reset=True) == 2
+        assert_attention(got, attention(cache, q, n, 0.1, window))
