@@ -3,7 +3,10 @@
 Every function forwards to the C ABI of the in-tree ``libtq.so``; all work runs
 in its CUDA kernels. Tensors are passed as raw pointers (``data_ptr()``), an
 ``int`` is taken as a raw pointer, ``None`` as NULL. ``stream`` defaults to
-PyTorch's current CUDA stream. A non-OK status raises :class:`TQError`.
+PyTorch's current CUDA stream. A non-OK status raises :class:`TQError`. The
+rotary and cache calls refuse tensors that the kernel would misread: of another
+type, on another device, or a view that is neither contiguous nor rows at the
+distance given.
 
 There is no fallback: if ``libtq.so`` is missing, every call raises (the
 package itself still imports, so that its ``build`` module can run). Build it

@@ -12,8 +12,10 @@
 // group of D/8 lanes holds one (token, head) pair of rows, 8 values of each
 // per lane with 16-byte loads, and the largest magnitude is a shuffle
 // reduction inside the group. Prompts of 13,400 tokens in all, 5 heads of
-// 128 in fp32 (77 MB), take 16.3 us, 4.7 TB/s: instructions are as near a bound
-// (issue slots 65% busy at 18.3 us, when whole rounds per CTA left some SMs short).
+// 128 in fp32 (77 MB), take 16.2 us from memory, 4.7 TB/s, and 14.9 where the
+// inputs of the call before are still in L2, with 65% of the issue slots busy: no
+// unit is full. bf16 rows of as many tokens, 43 MB, take 18.9 and 16.7: as many
+// instructions a value, 73% of the slots, with all of a CTA's start for each item.
 #include <algorithm>
 
 #include "kv4_common.cuh"

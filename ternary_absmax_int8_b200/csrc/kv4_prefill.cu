@@ -33,7 +33,7 @@
 // latencies of their own chain (scores from tensor memory, maximum, exponentials,
 // weights back). A CTA's start takes 9000 cycles (lengths, keys and queries from
 // memory, their expansion), its end 4500, the next CTA's arrival 1900. A prompt of
-// 8192 tokens (20 heads on 5, D = 128; 344 GFLOP) takes 367 us, 937 TFLOP/s, 57%
+// 8192 tokens (20 heads on 5, D = 128; 344 GFLOP) takes 365 us, 942 TFLOP/s, 57%
 // of a plain library product's rate (tensor pipe 39% busy, issue slots 51%,
 // exponentials 41% over 4096 tokens). What was tried, in us for that prompt:
 // scores of whole tiles, not ahead 519, of half tiles two ahead 422 (380 with all
@@ -1049,8 +1049,11 @@ struct PrefillPlan {
 // CTAs run one to an SM, so s parts of c units' tiles take ceil(c s / SMs)
 // turns of tiles / s each, and about four tiles' time for every turn's start,
 // end and joining; from two turns on, parts gain less than they cost. (Two
-// sequences of 512 tokens behind up to 16000, 5 heads of 4: 182, 162, 164, 160, 177, 175, 189, 207 us
-// with 2, 3, 4, 5, 6, 7, 9, 11 parts when 5 parts took 160; they take 152.5 now.)
+// sequences of 512 tokens behind up to 16000, 5 heads of 4: 238, 177, 156, 156,
+// 152, 167, 166, 174, 179, 195, 216 us with 1 to 9, 11 and 14 parts; 5 are taken.)
+// The host knows the table's width alone, not the lengths: in a table of 131072
+// tokens those two sequences get 17 parts and take 234 us, a prompt of 2048
+// tokens 12 parts and 192 us where its own width gives one part and 46.
 PrefillPlan plan_prefill(const Kv4View &c, int D, int q_heads, int T)
 {
     PrefillPlan d;

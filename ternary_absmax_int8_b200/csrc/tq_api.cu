@@ -596,7 +596,7 @@ tq_status tq_rope(const tq_rope_rows *rows, int n, const int32_t *pos, int64_t p
     }
     if (count == 0)
         return ok();
-    // units of one CTA (four tokens at most) are counted in 32 bits
+    // units of one CTA (two tokens at most) are counted in 32 bits
     if (heads * (head_dim / 8) > (1ll << 28))
         return fail(TQ_ERR_UNSUPPORTED, "%s: %lld heads of %d", fn, heads, head_dim);
     cudaError_t e = tq::launch_rope(r, count, pos, pos_stride, inv_freq, sections, n_axes, T,
