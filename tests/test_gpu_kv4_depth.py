@@ -10,8 +10,9 @@ another, fewer than 300 additions: 2^-14 of A, within the 2^-12 that stand there
 sums and exponentials. Prompts: at most 16,400 keys, 16 to an addition, in up to 32
 parts: 1060 additions of 2^-23 in the matrix unit, 2^-12.9 of A, and what the sum of
 weights loses (1 / 8 of that many additions, 2^-24 each, 2^-17): within 2^-12 as well.
-The logarithm of a sum of weights moves by their relative error: fewer than 200
-additions of 2^-24 one after another, 2^-16, for the 2^-18 of short sequences."""
+The logarithm of a sum of weights moves by its relative error: fewer than 250
+additions of 2^-24 one after another (8 a tile and lane, then lanes, warps, SMs),
+2^-16, for the 2^-18 of short sequences."""
 import math
 
 import numpy as np
