@@ -42,10 +42,11 @@
 //
 // Measured (20 heads on 5 of 128, pages of 64): one sequence of 777 tokens
 // 6.4 us; 24 of up to 8191 (65 MB) 22.1 us from memory, 2.9 TB/s, 20.4 with the
-// cache in L2; one of 262143 (173 MB) 38.1 us, 4.5 TB/s. Of the long call the start (lengths, page numbers, first
-// copies) takes 2.7 us, merge and join 4; between them it runs at 6 TB/s with
-// the issue slots 57%, ALUs 53% and matrix pipes 28% busy. The batch's tiles are
-// a third of that, and its start and end, with more joins, the same.
+// cache in L2; one of 262143 (173 MB) 38.1 us, 4.5 TB/s. Of the long call the
+// start (lengths, page numbers, first copies) takes 2.7 us, merge and join 4;
+// between them it runs at 6 TB/s with the issue slots 57%, ALUs 54% and matrix
+// pipes 28% busy. The batch's tiles are a third of that, and its start and end,
+// with more joins, the same.
 #include <algorithm>
 
 #include "kv4_common.cuh"

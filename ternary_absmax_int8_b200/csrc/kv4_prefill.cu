@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     if (warp < 8) {
         // ---------------------------------------------------------- softmax
         const int s = warp >> 2;
-        const int pos = real ? u.pos0 + tok : -1;  // -1: sees nothing
+        const int pos = real ? u.pos0 + tok : -1;  // below 0: sees nothing
         const int low = p.q.window > 0 ? pos - p.q.window + 1 : 0;  // first key seen
         // what all rows of the tile see: keys [low_max, pos_min]
         const int pos_min = u.pos0 + p.by_rep.of(u.row0 + s * 128);
